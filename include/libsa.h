@@ -1,5 +1,5 @@
 /*
- * libsa -- Stochastic Attention (SA) forward pass on NVIDIA GB300 (sm_103a).
+ * libsa -- Stochastic Attention (SA) on NVIDIA GB300 (sm_103a).
  *
  * What the library computes ("Stochastic Attention" technical summaries,
  * gist.science/ja/paper/2604.00754 and gist.science/ko/paper/2604.00754):
@@ -59,7 +59,8 @@ typedef enum sa_status {
   SA_ERR_INVALID_ARG = 1, /* NULL pointer, size <= 0, Hq % Hkv != 0, ... */
   SA_ERR_UNSUPPORTED = 2, /* valid request this library cannot run (head_dim, alignment, kernel) */
   SA_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed */
-  SA_ERR_BAD_PERM = 4,    /* device check found perm entries out of range or repeated */
+  SA_ERR_BAD_PERM = 4,    /* device check found entries out of range (perm, lengths, tables,
+                             slots) or repeated (perm) */
   SA_ERR_TIMEOUT = 5,     /* a device pipeline wait ran past its bound; results are invalid */
   SA_ERR_INTERNAL = 6     /* a device self-check of an internal index failed (a library bug) */
 } sa_status_t;
@@ -77,7 +78,7 @@ enum {
 };
 
 /* Bits of the device error word. */
-#define SA_ERRBIT_RANGE 1   /* a perm entry outside [0, seqlen) */
+#define SA_ERRBIT_RANGE 1   /* an entry out of range: perm, or a paged call's lengths, tables, slots */
 #define SA_ERRBIT_DUP 2     /* two positions of perm name the same token */
 #define SA_ERRBIT_TIMEOUT 4 /* a bounded pipeline wait gave up */
 #define SA_ERRBIT_INTERNAL 8 /* an internal index self-check failed (a library bug); access skipped */
@@ -311,10 +312,166 @@ sa_status_t sa_make_perm(uint64_t seed, int32_t layer, int32_t batch_index, int3
                          int32_t* perm_host);
 
 /*
+ * ------------------------------------------------------------------ serving
+ * SA and SWA layers over a paged K/V cache, for batches of requests that each
+ * bring one or many new tokens (decoding, chunked prompts, or both at once).
+ *
+ * A cache is two arrays of pages, k_cache and v_cache, bf16
+ *   [num_pages, page_size, num_kv_heads, head_dim],
+ * contiguous within a page.  Position j of request b lives in row
+ * j % page_size of page block_table[b, j / page_size].  Request b has
+ * seq_lens[b] tokens in all, the new ones included and already in the cache;
+ * its new tokens are the last n_b = q_start[b+1] - q_start[b] of them, and
+ * their rows of q, out and the gates are q_start[b] .. q_start[b+1] - 1 (the
+ * requests packed one after the other).  So row q_start[b] + i has position
+ * seq_lens[b] - n_b + i.
+ *
+ * Lengths, tables and sigma are device data and are checked on the device: a
+ * request whose numbers do not fit (n_b < 0, more than max_new or than
+ * seq_lens[b], rows outside [0, tokens), a length beyond its block table or
+ * beyond sigma) sets SA_ERRBIT_RANGE and its rows of out are left as they
+ * were; a key whose page or sigma entry is out of range sets SA_ERRBIT_RANGE
+ * and is not attended.  A row that attends nothing is 0.  Rows of q and out
+ * outside [q_start[0], q_start[batch]) are neither read nor written.  Cache
+ * rows that no attended position names are never used: they may hold anything.
+ */
+typedef struct sa_paged_params {
+  int32_t batch;         /* B >= 1 requests */
+  int32_t tokens;        /* T >= 0 rows of q and out */
+  int32_t max_new;       /* no request brings more new tokens than this; <= 0: T */
+  int32_t num_q_heads;   /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;  /* Hkv >= 1 */
+  int32_t head_dim;      /* d: 64 or 128 */
+  int32_t page_size;     /* tokens per page, >= 1 */
+  int32_t num_pages;     /* pages of the cache, >= 1; num_pages * page_size < 2^31 */
+  int32_t max_pages;     /* entries of one block table row, >= 1 */
+  int32_t window;        /* SA: half-width floor(window / 2); SWA: window keys (2^30 or more: all) */
+  int32_t window_swa;    /* gated call: SWA window; <= 0 means "same as window" */
+  int32_t perm_rows;     /* SA: rows of perm and inv_perm: B, or 1 shared by all requests */
+  int32_t perm_len;      /* SA: n, the length sigma was drawn for (>= every seq_lens[b]) */
+  int32_t kernel;        /* SA_PAGED_* */
+  float softmax_scale;   /* <= 0 means 1/sqrt(head_dim) */
+  int32_t reserved;      /* 0 */
+  int64_t q_stride;      /* elements between tokens of q; 0: num_q_heads * head_dim; a multiple of 8 */
+  int64_t page_stride;   /* elements between pages of either cache; 0: contiguous; a multiple of 8 */
+  const int32_t* block_table; /* device [B, max_pages] */
+  const int32_t* q_start;     /* device [B + 1] */
+  const int32_t* seq_lens;    /* device [B] */
+  int32_t* err;               /* device int32 error word, or NULL for the library's own */
+} sa_paged_params_t;
+
+/* Kernel choice (sa_paged_params_t.kernel). */
+enum {
+  SA_PAGED_AUTO = 0,  /* requests with few new rows on the row kernel, others on the tile kernel */
+  SA_PAGED_ROWS = 1,  /* row kernel for every request: warps stream the keys of up to 16 query rows */
+  SA_PAGED_TILES = 2  /* SWA: tcgen05 tiles of 256 query rows for every request;
+                         SA_ERR_UNSUPPORTED where they do not fit (num_q_heads / num_kv_heads
+                         must divide 32) */
+};
+
+/*
+ * Sliding-window attention over the cache ("Problem statement"): the token at
+ * position i attends to positions [max(0, i - window + 1), i].  q bf16
+ * [T, Hq, d] (tokens q_stride apart), out bf16 [T, Hq, d] contiguous.
+ * workspace: sa_paged_workspace_size bytes, 256-byte aligned, contents
+ * ignored on entry, not shared by calls that may overlap.  Asynchronous on
+ * `stream`, allocates nothing; may be captured into a graph, which then reads
+ * the lengths and tables of its replay.
+ */
+sa_status_t swa_paged_forward(const sa_paged_params_t* params, const void* q, const void* k_cache,
+                              const void* v_cache, void* out, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Causal Stochastic Attention over the cache ("Core mechanism" steps 1-3 with
+ * the causal rule of "Theoretical properties"): sigma = perm[b] is drawn once
+ * for perm_len tokens, the most the request may reach; the token at position
+ * i, p = inv_perm[b][i], attends to the tokens sigma[q] <= i with
+ * |q - p| <= floor(window / 2).  Because of the causal rule a row depends on
+ * the tokens up to its own alone: feeding a sequence of perm_len tokens in
+ * any chunks gives the rows of sa_forward on the whole of it.  perm and
+ * inv_perm: device int32 [perm_rows, perm_len].
+ */
+sa_status_t sa_paged_forward(const sa_paged_params_t* params, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* perm, const int32_t* inv_perm,
+                             void* out, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/*
+ * The gated dual path over the cache ("Gated SA and SWA" equation):
+ *   out = sigmoid(gate_sa_logits) * SA(window) + sigmoid(gate_swa_logits) * SWA(window_swa)
+ * with the gate logits fp32 [T, Hq] of the new tokens.  Both terms are summed
+ * in fp32 and rounded once.
+ */
+sa_status_t sa_swa_gated_paged_forward(const sa_paged_params_t* params, const void* q,
+                                       const void* k_cache, const void* v_cache,
+                                       const int32_t* perm, const int32_t* inv_perm,
+                                       const float* gate_sa_logits, const float* gate_swa_logits,
+                                       void* out, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/* Bytes of device workspace the three calls need for these params (path: 0
+ * swa_paged_forward, 1 sa_paged_forward, 2 sa_swa_gated_paged_forward); 0 for
+ * params the call would refuse.  Reads only the sizes. */
+size_t sa_paged_workspace_size(const sa_paged_params_t* params, int32_t path);
+
+/*
+ * Plan of one step, built on the device from the requests' lengths: request b
+ * holds cached_lens[b] tokens in the pages its block table row names and
+ * brings new_lens[b] more.  Pages it lacks are taken off the top of the free
+ * list (free_pages[num_free - 1], then downwards), in request order.
+ *   block_table  in/out int32 [batch, max_pages]: entries of the taken pages are written
+ *   q_start      out int32 [batch + 1]: first row of each request's new tokens
+ *   seq_lens     out int32 [batch]: cached + new
+ *   slots        out int32 [max_tokens]: page * page_size + row of each new token, -1 past the last
+ *   positions    out int32 [max_tokens]: position of each new token, -1 past the last
+ *   counts       out int32 [3]: new tokens in all, pages taken, pages left on the free list
+ * num_free: device int32 [1]; the next step's is counts[2].  All or nothing:
+ * negative lengths, a request longer than its block table, more tokens than
+ * max_tokens or more pages than are free set SA_ERRBIT_RANGE, give q_start 0,
+ * seq_lens = cached_lens, slots and positions -1, counts {0, 0, num_free},
+ * and leave the block table as it was.  A page id outside [0, num_pages) sets
+ * SA_ERRBIT_RANGE and gives its tokens the slot -1.  Outputs must not overlap
+ * inputs (block_table apart) or each other.  One launch, asynchronous.
+ */
+sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cached_lens, int32_t batch,
+                          int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                          int32_t free_capacity, const int32_t* num_free, int32_t page_size,
+                          int32_t num_pages, int32_t max_tokens, int32_t* q_start,
+                          int32_t* seq_lens, int32_t* slots, int32_t* positions, int32_t* counts,
+                          int32_t* d_err, cudaStream_t stream);
+
+/*
+ * New tokens into the cache: row slots[t] of the pages (page slots[t] /
+ * page_size) gets k[t] and v[t] (bf16 [tokens, num_kv_heads, head_dim],
+ * tokens k_stride and v_stride elements apart).  With rope_base > 1 the keys
+ * are rotated by positions[t] on the way, as sa_rope does, and q (bf16
+ * [tokens, num_q_heads, head_dim], q_stride apart; NULL for none) is rotated
+ * into q_out (contiguous, distinct from q); with rope_base 0 there is no
+ * rotation, and q and q_out must be NULL.  A slot of -1 (padding) writes
+ * nothing and leaves q_out's row; any other slot outside the cache, or a
+ * negative position, sets SA_ERRBIT_RANGE and is treated likewise.  Two tokens
+ * with one slot leave either's row.  head_dim even, <= 256; strides 0 mean
+ * contiguous.  Any 2-byte-aligned data; 16-byte-aligned rows with
+ * head_dim % 16 == 0 take the widest accesses.
+ */
+typedef struct sa_paged_append_params {
+  int32_t tokens, num_kv_heads, num_q_heads, head_dim;
+  int32_t page_size, num_pages;
+  int64_t k_stride, v_stride, q_stride; /* elements between tokens */
+  int64_t page_stride;                  /* elements between pages */
+  double rope_base;
+  int32_t* err;
+} sa_paged_append_params_t;
+sa_status_t sa_paged_append(const sa_paged_append_params_t* params, const void* k, const void* v,
+                            const void* q, const int32_t* slots, const int32_t* positions,
+                            void* k_cache, void* v_cache, void* q_out, cudaStream_t stream);
+
+/*
  * Synchronise `stream`, read the device error word (NULL: the library's own)
  * and map it to a status: SA_ERR_INTERNAL if SA_ERRBIT_INTERNAL is set, else
- * SA_ERR_TIMEOUT if SA_ERRBIT_TIMEOUT is set, else SA_ERR_BAD_PERM if a perm
- * bit is set, else SA_OK.  The word is left as is.
+ * SA_ERR_TIMEOUT if SA_ERRBIT_TIMEOUT is set, else SA_ERR_BAD_PERM if
+ * SA_ERRBIT_RANGE or SA_ERRBIT_DUP is set, else SA_OK.  The word is left as is.
  */
 sa_status_t sa_check_error(const int32_t* d_err, cudaStream_t stream);
 

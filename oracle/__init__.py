@@ -23,6 +23,8 @@ gist.science/ja/paper/2604.00754 and gist.science/ko/paper/2604.00754):
 * ``prologue``  -- the two gate projections of the layer input and the
                   rotary position embedding by original token index that
                   feed the attention paths ("Gated SA and SWA" section).
+* ``paged``     -- the same attention rows over a paged K/V cache, the plan of a
+                  serving step and the writer of its new tokens.
 * ``graph``     -- neighbour sets, the pairwise connection probability and the
                   receptive-field growth over stacked layers
                   (section "Core mechanism", last paragraph; "Theoretical
@@ -52,6 +54,7 @@ from .backward import (
     sa_lse,
     swa_lse,
 )
+from .paged import paged_attention, paged_plan, rotate_at
 from .prologue import gate_logits, rope, rope_angles
 from .graph import (
     neighbours_sa,
@@ -78,6 +81,9 @@ __all__ = [
     "gated_forward",
     "full_attention",
     "masked_attention",
+    "paged_attention",
+    "paged_plan",
+    "rotate_at",
     "gate_logits",
     "rope",
     "rope_angles",

@@ -2,8 +2,9 @@
 
 Python face of the ``libsa`` C-ABI library (include/libsa.h): SA over a
 seeded random permutation of the tokens, sliding-window attention, the
-sigmoid-gated SA+SWA merge and the device inverse permutation, each running
-in hand-written CUDA kernels.  PyTorch supplies device memory and streams.
+sigmoid-gated SA+SWA merge, the device inverse permutation, and the same
+attention over a paged K/V cache for serving, each running in hand-written CUDA
+kernels.  PyTorch supplies device memory and streams.
 """
 
 from ._libsa import (
@@ -47,6 +48,19 @@ from ._libsa import (
     swa_backward,
     swa_forward,
 )
+from ._paged import (
+    PAGED_AUTO,
+    PAGED_ROWS,
+    PAGED_TILES,
+    PagedPlan,
+    SaPagedAppendParams,
+    SaPagedParams,
+    paged_append,
+    paged_plan,
+    sa_paged_forward,
+    sa_swa_gated_paged_forward,
+    swa_paged_forward,
+)
 
 __all__ = [
     "ERRBIT_DUP", "ERRBIT_INTERNAL", "ERRBIT_RANGE", "ERRBIT_TIMEOUT", "KERNEL_AUTO", "KERNEL_SIMT", "KERNEL_TCGEN05", "KERNEL_TCGEN05_GATHER", "KERNEL_TCGEN05_RING", "KERNEL_TCGEN05_CHUNK",
@@ -56,4 +70,7 @@ __all__ = [
     "sa_swa_gated_forward", "set_wait_limit", "get_wait_limit", "swa_forward",
     "sa_backward", "swa_backward", "sa_swa_gated_backward", "receptive_field",
     "gate_projection", "rope_",
+    "PAGED_AUTO", "PAGED_ROWS", "PAGED_TILES", "PagedPlan", "SaPagedAppendParams", "SaPagedParams",
+    "paged_append", "paged_plan", "sa_paged_forward", "sa_swa_gated_paged_forward",
+    "swa_paged_forward",
 ]

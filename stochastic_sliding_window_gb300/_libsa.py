@@ -44,6 +44,13 @@ SIGNATURES = {
     "sa_receptive_field_workspace_size": (c_size_t, [c_int32]),
     "sa_receptive_field": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p,
                                      c_int32, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "swa_paged_forward": (c_int32, [c_void_p] * 6 + [c_size_t, c_void_p]),
+    "sa_paged_forward": (c_int32, [c_void_p] * 8 + [c_size_t, c_void_p]),
+    "sa_swa_gated_paged_forward": (c_int32, [c_void_p] * 10 + [c_size_t, c_void_p]),
+    "sa_paged_workspace_size": (c_size_t, [c_void_p, c_int32]),
+    "sa_paged_plan": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int32,
+                                c_void_p, c_int32, c_int32, c_int32] + [c_void_p] * 7),
+    "sa_paged_append": (c_int32, [c_void_p] * 10),
     "sa_make_perm": (c_int32, [c_uint64, c_int32, c_int32, c_int32, POINTER(c_int32)]),
     "sa_shard_span": (c_int32, [c_int32, c_int32, c_int32, c_int32]),
     "sa_shard_plan": (c_int32, [POINTER(c_int32), c_int32, c_int32, c_int32, c_int32,

@@ -33,6 +33,11 @@ sa_status_t fail(sa_status_t st, const char* fmt, ...) {
   return st;
 }
 
+sa_status_t succeed() {
+  g_msg[0] = '\0';
+  return SA_OK;
+}
+
 int32_t* default_error_word() {
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_error_word) != cudaSuccess) return nullptr;
@@ -526,7 +531,8 @@ extern "C" sa_status_t sa_check_error(const int32_t* d_err, cudaStream_t stream)
     return fail(SA_ERR_INTERNAL, "a device self-check of an internal index failed");
   if (host & SA_ERRBIT_TIMEOUT) return fail(SA_ERR_TIMEOUT, "a device wait ran past its bound");
   if (host & (SA_ERRBIT_RANGE | SA_ERRBIT_DUP))
-    return fail(SA_ERR_BAD_PERM, "perm is not a permutation (error bits 0x%x)", host);
+    return fail(SA_ERR_BAD_PERM, "perm is not a permutation, or a paged call's lengths, tables or "
+                "slots are out of range (error bits 0x%x)", host);
   return SA_OK;
 }
 
@@ -552,7 +558,7 @@ extern "C" const char* sa_status_string(sa_status_t status) {
     case SA_ERR_INVALID_ARG: return "SA_ERR_INVALID_ARG: invalid argument";
     case SA_ERR_UNSUPPORTED: return "SA_ERR_UNSUPPORTED: not supported by this library";
     case SA_ERR_CUDA: return "SA_ERR_CUDA: CUDA runtime error";
-    case SA_ERR_BAD_PERM: return "SA_ERR_BAD_PERM: perm is not a permutation";
+    case SA_ERR_BAD_PERM: return "SA_ERR_BAD_PERM: perm, lengths, tables or slots out of range";
     case SA_ERR_TIMEOUT: return "SA_ERR_TIMEOUT: device wait ran past its bound";
     case SA_ERR_INTERNAL: return "SA_ERR_INTERNAL: device self-check failed";
   }

@@ -38,6 +38,9 @@ struct Problem {
 // Record a detail message for sa_last_error_message() and return `st`.
 sa_status_t fail(sa_status_t st, const char* fmt, ...);
 
+// Clear that message and return SA_OK.
+sa_status_t succeed();
+
 // Device error word owned by the library (used when the caller passes NULL).
 int32_t* default_error_word();
 
@@ -109,6 +112,36 @@ sa_status_t launch_gate_projection(const void* x, int tokens, int d_model, int h
                                    float* a_sa, float* a_swa, int32_t* err, cudaStream_t stream);
 sa_status_t launch_rope(void* x, int batch, int n, int heads, int head_dim, double base,
                         cudaStream_t stream);
+
+// Attention over a paged cache, already validated on the host.
+struct PagedProblem {
+  int B, T, max_new, Hq, Hkv, d, g;
+  int page, num_pages, max_pages;
+  int window_swa;            // SWA window (swa and gated paths)
+  int half;                  // SA half-width (sa and gated paths)
+  int perm_rows, perm_len;
+  float scale;
+  long long q_stride, page_stride;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* seq_lens;
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* perm;
+  const int32_t* inv;
+  const float* gate_sa;      // [T, Hq] logits (gated path)
+  const float* gate_swa;
+  void* out;
+  int32_t* err;
+};
+
+// Row kernel (sa_paged_rows.cu).  Requests with more than row_limit new
+// tokens are skipped (swa path), or take their SWA term from swa_part, fp32
+// [T, Hq, d], gate applied (gated path).  `part`: the workspace.
+size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int sms);
+sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
+                              const float* swa_part, void* part, int sms, cudaStream_t stream);
 
 // sigma^{-1} kernels.
 sa_status_t launch_inverse_perm(const int32_t* perm, int32_t* inv, int batch, int n,

@@ -1,0 +1,621 @@
+// Serving over a paged K/V cache: the C-ABI entry points, the plan of a step
+// (block tables, slots and positions from the requests' lengths) and the
+// writer of new keys and values.  The attention itself is in
+// sa_paged_rows.cu.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "sa_internal.h"
+
+namespace sa {
+namespace paged {
+
+// ------------------------------------------------------------------ plan
+//
+// q_start = exclusive sum of n_b, and the pages request b takes are the
+// exclusive sum S_b of need_b = ceil((c_b + n_b) / P) - ceil(c_b / P), so
+// token i of request b (position p = c_b + i, table column p / P) lies in the
+// page that column held before, or, past the owned columns, in
+// free[num_free - 1 - (S_b + column - owned_b)].  Nothing is read back from
+// what is written, so one launch does it: every block scans all lengths (a few
+// KB from L2) and then places its own kTokens tokens by a binary search among
+// the request starts in shared memory.  A page that is taken always begins
+// with a new token, whose thread writes the table entry.
+//
+// Bound by latency: two passes over the lengths (check, then scan), a search
+// and two dependent loads, then one 8-byte store per token.
+
+constexpr int kPlanThreads = 512;
+constexpr int kTokens = 1024;  // tokens per block
+
+struct PlanParams {
+  const int32_t* new_lens;
+  const int32_t* cached;
+  const int32_t* free_pages;
+  const int32_t* num_free;
+  int32_t* table;
+  int32_t* q_start;
+  int32_t* seq_lens;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* counts;
+  int32_t* err;
+  int B, max_pages, free_capacity, page, num_pages, max_tokens;
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) sa_paged_plan_kernel(const __grid_constant__ PlanParams P) {
+  __shared__ long long s_sum[2][kPlanThreads / 32];
+  __shared__ int s_scan[2][kPlanThreads / 32];
+  __shared__ int s_start[kPlanThreads + 1], s_take[kPlanThreads];
+  __shared__ int s_cached[kPlanThreads], s_row[kPlanThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int page = P.page;
+  const int nfree = *P.num_free;
+  // check: totals in 64 bits
+  long long tokens = 0, pages = 0;
+  int bad = nfree < 0 || nfree > P.free_capacity;
+  for (int b = tid; b < P.B; b += kPlanThreads) {
+    const int n = P.new_lens[b], c = P.cached[b];
+    const long long len = (long long)n + c;
+    if (n < 0 || c < 0 || len > (long long)P.max_pages * page || len > 2147483647LL) {
+      bad = 1;
+    } else {
+      tokens += n;
+      pages += (len + page - 1) / page - (c + (long long)page - 1) / page;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  tokens = warp_sum(tokens);
+  pages = warp_sum(pages);
+  if (lane == 0) {
+    s_sum[0][warp] = tokens;
+    s_sum[1][warp] = pages;
+  }
+  __syncthreads();
+  tokens = pages = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    tokens += s_sum[0][w];
+    pages += s_sum[1][w];
+  }
+  if (bad || tokens > P.max_tokens || pages > nfree) {  // uniform over the grid
+    if (blockIdx.x == 0) {
+      for (int b = tid; b < P.B; b += kPlanThreads) P.seq_lens[b] = P.cached[b];
+      for (int b = tid; b <= P.B; b += kPlanThreads) P.q_start[b] = 0;
+      if (tid == 0) {
+        P.counts[0] = 0;
+        P.counts[1] = 0;
+        P.counts[2] = nfree;
+        atomicOr(P.err, SA_ERRBIT_RANGE);
+      }
+    }
+    for (int t = blockIdx.x * kTokens + tid; t < min(P.max_tokens, int(blockIdx.x + 1) * kTokens); t += kPlanThreads) {
+      P.slots[t] = -1;
+      P.positions[t] = -1;
+    }
+    return;
+  }
+  const int t0 = blockIdx.x * kTokens, t1 = min(P.max_tokens, t0 + kTokens);
+  int base = 0, pbase = 0;  // tokens and pages of the requests before this chunk
+  for (int b0 = 0, chunk = 0; b0 < P.B; b0 += kPlanThreads, ++chunk) {
+    const bool writer = chunk % int(gridDim.x) == int(blockIdx.x);
+    const int b = b0 + tid;
+    int n = 0, c = 0, take = 0;
+    if (b < P.B) {
+      n = P.new_lens[b];
+      c = P.cached[b];
+      take = int((unsigned(c) + unsigned(n) + unsigned(page) - 1u) / unsigned(page) -
+                 (unsigned(c) + unsigned(page) - 1u) / unsigned(page));
+    }
+    int sn = n, st = take;  // inclusive scans
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, sn, o), d = __shfl_up_sync(0xffffffffu, st, o);
+      if (lane >= o) {
+        sn += a;
+        st += d;
+      }
+    }
+    __syncthreads();  // the previous chunk's searches are done
+    if (lane == 31) {
+      s_scan[0][warp] = sn;
+      s_scan[1][warp] = st;
+    }
+    __syncthreads();
+    int tn = 0, tt = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) {
+        sn += s_scan[0][w];
+        st += s_scan[1][w];
+      }
+      tn += s_scan[0][w];
+      tt += s_scan[1][w];
+    }
+    s_start[tid + 1] = base + sn;
+    if (tid == 0) s_start[0] = base;
+    s_take[tid] = pbase + st - take;
+    s_cached[tid] = c;
+    s_row[tid] = b;
+    if (writer && b < P.B) {
+      P.q_start[b + 1] = base + sn;
+      P.seq_lens[b] = c + n;
+      if (b == 0) P.q_start[0] = 0;
+    }
+    __syncthreads();
+    const int end = base + tn;
+    for (int t = max(t0, base) + tid; t < min(t1, end); t += kPlanThreads) {
+      int lo = 0, hi = kPlanThreads - 1;  // the last request that starts at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_start[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int cc = s_cached[lo], pos = cc + (t - s_start[lo]);
+      const int col = int(unsigned(pos) / unsigned(page)), in = pos - col * page;
+      const int owned = int((unsigned(cc) + unsigned(page) - 1u) / unsigned(page));
+      int32_t* entry = P.table + (long long)s_row[lo] * P.max_pages + col;
+      const int id = col < owned ? *entry : P.free_pages[nfree - 1 - (s_take[lo] + col - owned)];
+      if (col >= owned && in == 0) *entry = id;
+      const bool ok = unsigned(id) < unsigned(P.num_pages);
+      if (!ok) atomicOr(P.err, SA_ERRBIT_RANGE);
+      P.slots[t] = ok ? id * page + in : -1;
+      P.positions[t] = pos;
+    }
+    base = end;
+    pbase += tt;
+  }
+  for (int t = max(t0, base) + tid; t < t1; t += kPlanThreads) {
+    P.slots[t] = -1;
+    P.positions[t] = -1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    P.counts[0] = base;
+    P.counts[1] = pbase;
+    P.counts[2] = nfree - pbase;
+  }
+}
+
+// ------------------------------------------------------------------ append
+//
+// A copy with a rotation on the way: each (token, head) row of q, k and v is
+// read once and written once.  Bound by HBM.  A thread takes 8 pairs
+// (x_k, x_{k + d/2}) of one head, two 16-byte loads and two 16-byte stores;
+// several items per thread are loaded before the block's angles are computed.
+// The angle of position p at frequency f_k = base^(-2k/d) / (2 pi) turns per
+// token is p f_k mod 1: with f_k as a 64-bit fraction of a turn the product
+// wraps by itself, exact to p 2^-64 of a turn, and its top 32 bits give the
+// angle to 2^-32 of a turn -- no 64-bit floating point, any position.
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendPre = 4;       // items per thread loaded before the angles
+constexpr int kMaxAngles = 1024;    // angle slots per block
+
+struct AppendParams {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* q;
+  const int32_t* slots;
+  const int32_t* positions;
+  __nv_bfloat16* kc;
+  __nv_bfloat16* vc;
+  __nv_bfloat16* qo;
+  int32_t* err;
+  long long ks, vs, qs, page_stride;
+  int T, Hkv, Hq, d, page;
+  int rows_end;  // num_pages * page_size
+  int rope;
+  int tpb;       // tokens per block
+  uint64_t freq[128];  // turns per token, as fractions of 2^64
+};
+
+struct AppendRow {
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;
+  int rot;
+};
+
+// Where head row `hh` of token t (its cache row at `slot`) comes from and goes.
+__device__ __forceinline__ AppendRow append_row(const AppendParams& P, int t, int slot, int hh) {
+  AppendRow r;
+  if (hh >= 2 * P.Hkv) {
+    const int h = hh - 2 * P.Hkv;
+    r.src = P.q + (long long)t * P.qs + h * P.d;
+    r.dst = P.qo + ((long long)t * P.Hq + h) * P.d;
+    r.rot = 1;
+    return r;
+  }
+  const int isv = hh >= P.Hkv, h = hh - (isv ? P.Hkv : 0);
+  const int pg = int(unsigned(slot) / unsigned(P.page)), in = slot - pg * P.page;
+  const long long at = (long long)pg * P.page_stride + ((long long)in * P.Hkv + h) * P.d;
+  r.src = isv ? P.v + (long long)t * P.vs + h * P.d : P.k + (long long)t * P.ks + h * P.d;
+  r.dst = (isv ? P.vc : P.kc) + at;
+  r.rot = P.rope && !isv;
+  return r;
+}
+
+// Slot of token t, or -1 where nothing is to be written.
+__device__ __forceinline__ int append_slot(const AppendParams& P, int t) {
+  const int slot = P.slots[t];
+  if (slot == -1) return -1;
+  if (unsigned(slot) >= unsigned(P.rows_end) || (P.rope && P.positions[t] < 0)) {
+    atomicOr(P.err, SA_ERRBIT_RANGE);
+    return -1;
+  }
+  return slot;
+}
+
+template <bool kVec>
+__global__ void __launch_bounds__(kAppendThreads) sa_paged_append_kernel(const __grid_constant__ AppendParams P) {
+  __shared__ float2 s_cs[kMaxAngles];
+  const int half = P.d / 2;
+  const int t0 = blockIdx.x * P.tpb;
+  const int ntok = min(P.tpb, P.T - t0);
+  const int per_head = kVec ? half / 8 : half;
+  const int heads = 2 * P.Hkv + P.Hq;
+  const int per_tok = heads * per_head;
+  const int items = ntok * per_tok;
+  auto angles = [&]() {
+    for (int a = threadIdx.x; a < ntok * half; a += kAppendThreads) {
+      const int tk = a / half, k = a - tk * half;
+      const uint64_t turns = P.freq[k] * uint64_t(uint32_t(P.positions[t0 + tk]));
+      const float x = float(int32_t(uint32_t(turns >> 32))) * 0x1p-31f;  // half turns in [-1, 1]
+      float s, c;
+      sincospif(x, &s, &c);
+      s_cs[a] = make_float2(c, s);
+    }
+    __syncthreads();
+  };
+  if constexpr (kVec) {
+    uint4 lo[kAppendPre], hi[kAppendPre];
+    AppendRow row[kAppendPre];
+    int ang[kAppendPre];
+    auto fetch = [&](int idx, int u) {
+      row[u].dst = nullptr;
+      if (idx >= items) return;
+      const int tk = idx / per_tok, rem = idx - tk * per_tok;
+      const int hh = rem / per_head, k = (rem - hh * per_head) * 8;
+      const int slot = append_slot(P, t0 + tk);
+      if (slot < 0) return;
+      row[u] = append_row(P, t0 + tk, slot, hh);
+      row[u].dst += k;
+      ang[u] = tk * half + k;
+      lo[u] = *reinterpret_cast<const uint4*>(row[u].src + k);
+      hi[u] = *reinterpret_cast<const uint4*>(row[u].src + k + half);
+    };
+    for (int i0 = 0; i0 < items; i0 += kAppendPre * kAppendThreads) {
+#pragma unroll
+      for (int u = 0; u < kAppendPre; ++u) fetch(i0 + u * kAppendThreads + threadIdx.x, u);
+      if (i0 == 0 && P.rope) angles();
+#pragma unroll
+      for (int u = 0; u < kAppendPre; ++u) {
+        if (row[u].dst == nullptr) continue;
+        if (row[u].rot) {
+          uint32_t* pl = reinterpret_cast<uint32_t*>(&lo[u]);
+          uint32_t* ph = reinterpret_cast<uint32_t*>(&hi[u]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            __nv_bfloat162 bl = *reinterpret_cast<__nv_bfloat162*>(&pl[e]);
+            __nv_bfloat162 bh = *reinterpret_cast<__nv_bfloat162*>(&ph[e]);
+            const float2 l = __bfloat1622float2(bl), h = __bfloat1622float2(bh);
+            const float2 a0 = s_cs[ang[u] + 2 * e], a1 = s_cs[ang[u] + 2 * e + 1];
+            bl = __floats2bfloat162_rn(l.x * a0.x - h.x * a0.y, l.y * a1.x - h.y * a1.y);
+            bh = __floats2bfloat162_rn(h.x * a0.x + l.x * a0.y, h.y * a1.x + l.y * a1.y);
+            pl[e] = *reinterpret_cast<uint32_t*>(&bl);
+            ph[e] = *reinterpret_cast<uint32_t*>(&bh);
+          }
+        }
+        *reinterpret_cast<uint4*>(row[u].dst) = lo[u];
+        *reinterpret_cast<uint4*>(row[u].dst + half) = hi[u];
+      }
+    }
+  } else {
+    if (P.rope) angles();
+    for (int idx = threadIdx.x; idx < items; idx += kAppendThreads) {
+      const int tk = idx / per_tok, rem = idx - tk * per_tok;
+      const int hh = rem / per_head, k = rem - hh * per_head;
+      const int slot = append_slot(P, t0 + tk);
+      if (slot < 0) continue;
+      const AppendRow r = append_row(P, t0 + tk, slot, hh);
+      __nv_bfloat16 lo = r.src[k], hi = r.src[k + half];
+      if (r.rot) {
+        const float l = __bfloat162float(lo), h = __bfloat162float(hi);
+        const float2 a = s_cs[tk * half + k];
+        lo = __float2bfloat16_rn(l * a.x - h * a.y);
+        hi = __float2bfloat16_rn(h * a.x + l * a.y);
+      }
+      r.dst[k] = lo;
+      r.dst[k + half] = hi;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// SM count of the current device, 0 unless it is an sm_103.
+static int sm103_sms() {
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 3) return 0;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+static sa_status_t check_sizes(const sa_paged_params_t* p, Path path) {
+  if (p == nullptr) return fail(SA_ERR_INVALID_ARG, "params is NULL");
+  if (p->batch < 1 || p->tokens < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1)
+    return fail(SA_ERR_INVALID_ARG, "batch and head counts must be >= 1, tokens >= 0");
+  if (p->num_q_heads % p->num_kv_heads != 0)
+    return fail(SA_ERR_INVALID_ARG, "num_q_heads (%d) must be a multiple of num_kv_heads (%d)",
+                p->num_q_heads, p->num_kv_heads);
+  if (p->head_dim != 64 && p->head_dim != 128)
+    return fail(SA_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", p->head_dim);
+  if (p->page_size < 1 || p->num_pages < 1 || p->max_pages < 1)
+    return fail(SA_ERR_INVALID_ARG, "page_size, num_pages and max_pages must be >= 1");
+  if (double(p->num_pages) * p->page_size >= 2147483648.0)
+    return fail(SA_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+  if (p->window < 1) return fail(SA_ERR_INVALID_ARG, "window must be >= 1");
+  if (p->kernel < SA_PAGED_AUTO || p->kernel > SA_PAGED_TILES)
+    return fail(SA_ERR_INVALID_ARG, "unknown kernel selector %d", p->kernel);
+  const long long row = (long long)p->num_q_heads * p->head_dim;
+  const long long page_elems = (long long)p->page_size * p->num_kv_heads * p->head_dim;
+  if ((p->q_stride != 0 && p->q_stride < row) || p->q_stride % 8 != 0)
+    return fail(SA_ERR_INVALID_ARG, "q_stride must be 0, or a multiple of 8 and at least %lld", row);
+  if ((p->page_stride != 0 && p->page_stride < page_elems) || p->page_stride % 8 != 0)
+    return fail(SA_ERR_INVALID_ARG, "page_stride must be 0, or a multiple of 8 and at least %lld",
+                page_elems);
+  if (double(p->tokens) * p->num_q_heads >= 2147483647.0)
+    return fail(SA_ERR_UNSUPPORTED, "tokens * num_q_heads too large");
+  if (path != kPathSWA) {
+    if (p->perm_len < 1 || (p->perm_rows != 1 && p->perm_rows != p->batch))
+      return fail(SA_ERR_INVALID_ARG, "perm_len must be >= 1, perm_rows 1 or batch");
+    if (p->kernel == SA_PAGED_TILES)
+      return fail(SA_ERR_UNSUPPORTED, "the tile kernel alone runs swa_paged_forward only");
+  }
+  return SA_OK;
+}
+
+static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
+  PagedProblem pb;
+  std::memset(&pb, 0, sizeof(pb));
+  pb.B = p->batch;
+  pb.T = p->tokens;
+  pb.max_new = p->max_new > 0 && p->max_new < p->tokens ? p->max_new : p->tokens;
+  pb.Hq = p->num_q_heads;
+  pb.Hkv = p->num_kv_heads;
+  pb.d = p->head_dim;
+  pb.g = pb.Hq / pb.Hkv;
+  pb.page = p->page_size;
+  pb.num_pages = p->num_pages;
+  pb.max_pages = p->max_pages;
+  pb.window_swa = path == kPathGated && p->window_swa > 0 ? p->window_swa : p->window;
+  pb.half = p->window / 2;
+  pb.perm_rows = p->perm_rows;
+  pb.perm_len = p->perm_len;
+  pb.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(float(pb.d));
+  pb.q_stride = p->q_stride ? p->q_stride : (long long)pb.Hq * pb.d;
+  pb.page_stride = p->page_stride ? p->page_stride : (long long)pb.page * pb.Hkv * pb.d;
+  pb.table = p->block_table;
+  pb.q_start = p->q_start;
+  pb.seq_lens = p->seq_lens;
+  return pb;
+}
+
+static size_t workspace_bytes(const PagedProblem& pb, Path path, int sms) {
+  return paged_rows_workspace_bytes(pb, path, sms);
+}
+
+static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, const void* k,
+                       const void* v, const int32_t* perm, const int32_t* inv,
+                       const float* gate_sa, const float* gate_swa, void* out, void* ws,
+                       size_t ws_bytes, cudaStream_t stream) {
+  sa_status_t st = check_sizes(prm, path);
+  if (st != SA_OK) return st;
+  if (prm->tokens == 0) return succeed();  // nothing to compute: empty tensors have no address
+  if (!q || !k || !v || !out || !prm->block_table || !prm->q_start || !prm->seq_lens)
+    return fail(SA_ERR_INVALID_ARG, "q, caches, out, block_table, q_start and seq_lens must be non-NULL");
+  if (path != kPathSWA && (!perm || !inv))
+    return fail(SA_ERR_INVALID_ARG, "perm and inv_perm must be non-NULL");
+  if (path == kPathGated && (!gate_sa || !gate_swa))
+    return fail(SA_ERR_INVALID_ARG, "both gate logit arrays must be non-NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+    return fail(SA_ERR_INVALID_ARG, "q, the caches and out must be 16-byte aligned");
+  if (out == q || out == k || out == v) return fail(SA_ERR_INVALID_ARG, "out aliases an input");
+  const int sms = sm103_sms();
+  if (sms == 0) return fail(SA_ERR_UNSUPPORTED, "device is not sm_103");
+  PagedProblem pb = make_problem(prm, path);
+  const size_t need = workspace_bytes(pb, path, sms);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(SA_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+  if (need > 0 && !aligned(ws, 256))
+    return fail(SA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  pb.q = q;
+  pb.k = k;
+  pb.v = v;
+  pb.perm = perm;
+  pb.inv = inv;
+  pb.gate_sa = gate_sa;
+  pb.gate_swa = gate_swa;
+  pb.out = out;
+  pb.err = prm->err ? prm->err : default_error_word();
+  if (!pb.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  if (prm->kernel == SA_PAGED_TILES) return fail(SA_ERR_UNSUPPORTED, "no tile kernel for this shape");
+  st = launch_paged_rows(pb, path, 0x7fffffff, nullptr, ws, sms, stream);
+  return st == SA_OK ? succeed() : st;
+}
+
+}  // namespace paged
+}  // namespace sa
+
+using namespace sa;
+
+extern "C" sa_status_t swa_paged_forward(const sa_paged_params_t* params, const void* q,
+                                         const void* k_cache, const void* v_cache, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         cudaStream_t stream) {
+  return paged::run(params, kPathSWA, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, out,
+                    workspace, workspace_bytes, stream);
+}
+
+extern "C" sa_status_t sa_paged_forward(const sa_paged_params_t* params, const void* q,
+                                        const void* k_cache, const void* v_cache,
+                                        const int32_t* perm, const int32_t* inv_perm, void* out,
+                                        void* workspace, size_t workspace_bytes,
+                                        cudaStream_t stream) {
+  return paged::run(params, kPathSA, q, k_cache, v_cache, perm, inv_perm, nullptr, nullptr, out,
+                    workspace, workspace_bytes, stream);
+}
+
+extern "C" sa_status_t sa_swa_gated_paged_forward(
+    const sa_paged_params_t* params, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* perm, const int32_t* inv_perm, const float* gate_sa_logits,
+    const float* gate_swa_logits, void* out, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream) {
+  return paged::run(params, kPathGated, q, k_cache, v_cache, perm, inv_perm, gate_sa_logits,
+                    gate_swa_logits, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t sa_paged_workspace_size(const sa_paged_params_t* params, int32_t path) {
+  if (path < 0 || path > 2) return 0;
+  const Path pt = path == 0 ? kPathSWA : path == 1 ? kPathSA : kPathGated;
+  if (paged::check_sizes(params, pt) != SA_OK || params->tokens == 0) return 0;
+  const int sms = paged::sm103_sms();
+  if (sms == 0) return 0;
+  return paged::workspace_bytes(paged::make_problem(params, pt), pt, sms);
+}
+
+extern "C" sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cached_lens,
+                                     int32_t batch, int32_t* block_table, int32_t max_pages,
+                                     const int32_t* free_pages, int32_t free_capacity,
+                                     const int32_t* num_free, int32_t page_size, int32_t num_pages,
+                                     int32_t max_tokens, int32_t* q_start, int32_t* seq_lens,
+                                     int32_t* slots, int32_t* positions, int32_t* counts,
+                                     int32_t* d_err, cudaStream_t stream) {
+  if (batch < 1 || max_pages < 1 || page_size < 1 || num_pages < 1 || max_tokens < 0 || free_capacity < 0)
+    return fail(SA_ERR_INVALID_ARG, "batch, max_pages, page_size and num_pages must be >= 1, "
+                "max_tokens and free_capacity >= 0");
+  if (!new_lens || !cached_lens || !block_table || !num_free || !q_start || !seq_lens || !counts ||
+      (max_tokens > 0 && (!slots || !positions)) || (free_capacity > 0 && !free_pages))
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (seq_lens == cached_lens || seq_lens == new_lens || q_start == new_lens ||
+      q_start == cached_lens || counts == num_free)
+    return fail(SA_ERR_INVALID_ARG, "an output aliases an input");
+  if (double(num_pages) * page_size >= 2147483648.0)
+    return fail(SA_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+  if (max_tokens > 2147483647 - paged::kTokens || page_size > (1 << 30))
+    return fail(SA_ERR_UNSUPPORTED, "max_tokens or page_size too large");
+  paged::PlanParams P;
+  P.new_lens = new_lens;
+  P.cached = cached_lens;
+  P.free_pages = free_pages;
+  P.num_free = num_free;
+  P.table = block_table;
+  P.q_start = q_start;
+  P.seq_lens = seq_lens;
+  P.slots = slots;
+  P.positions = positions;
+  P.counts = counts;
+  P.err = d_err ? d_err : default_error_word();
+  if (!P.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  P.B = batch;
+  P.max_pages = max_pages;
+  P.free_capacity = free_capacity;
+  P.page = page_size;
+  P.num_pages = num_pages;
+  P.max_tokens = max_tokens;
+  const int grid = max_tokens > paged::kTokens ? (max_tokens + paged::kTokens - 1) / paged::kTokens : 1;
+  paged::sa_paged_plan_kernel<<<grid, paged::kPlanThreads, 0, stream>>>(P);
+  const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(ce));
+  return succeed();
+}
+
+extern "C" sa_status_t sa_paged_append(const sa_paged_append_params_t* p, const void* k,
+                                       const void* v, const void* q, const int32_t* slots,
+                                       const int32_t* positions, void* k_cache, void* v_cache,
+                                       void* q_out, cudaStream_t stream) {
+  using namespace paged;
+  if (p == nullptr) return fail(SA_ERR_INVALID_ARG, "params is NULL");
+  if (p->tokens < 0 || p->num_kv_heads < 1 || p->num_q_heads < 0 || p->page_size < 1 ||
+      p->num_pages < 1 || p->head_dim < 2 || p->head_dim % 2 != 0 || p->head_dim > 256)
+    return fail(SA_ERR_INVALID_ARG, "need tokens >= 0, num_kv_heads, page_size, num_pages >= 1 and "
+                "an even head_dim <= 256");
+  if (double(p->num_pages) * p->page_size >= 2147483648.0)
+    return fail(SA_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+  const bool rope = p->rope_base != 0.0;
+  if (rope && !(p->rope_base > 1.0)) return fail(SA_ERR_INVALID_ARG, "rope_base must be 0 or > 1");
+  const bool with_q = q != nullptr || q_out != nullptr;
+  if (with_q && !rope) return fail(SA_ERR_INVALID_ARG, "q is rotated only: it needs rope_base");
+  const int d = p->head_dim, hq = with_q ? p->num_q_heads : 0, hkv = p->num_kv_heads;
+  if (with_q && hq < 1) return fail(SA_ERR_INVALID_ARG, "num_q_heads must be >= 1 when q is given");
+  if (2.0 * hkv + hq > 65536.0) return fail(SA_ERR_UNSUPPORTED, "too many heads");
+  if (p->tokens == 0) return succeed();
+  if (!k || !v || !slots || !k_cache || !v_cache || (rope && !positions) || (with_q && (!q || !q_out)))
+    return fail(SA_ERR_INVALID_ARG, "NULL pointer");
+  if (q_out != nullptr && (q_out == q || q_out == k || q_out == v))
+    return fail(SA_ERR_INVALID_ARG, "q_out aliases an input");
+  if (k_cache == v_cache || k_cache == k || v_cache == v)
+    return fail(SA_ERR_INVALID_ARG, "a cache aliases an input or the other cache");
+  AppendParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.ks = p->k_stride ? p->k_stride : (long long)hkv * d;
+  P.vs = p->v_stride ? p->v_stride : (long long)hkv * d;
+  P.qs = p->q_stride ? p->q_stride : (long long)hq * d;
+  P.page_stride = p->page_stride ? p->page_stride : (long long)p->page_size * hkv * d;
+  if (P.ks < (long long)hkv * d || P.vs < (long long)hkv * d || P.qs < (long long)hq * d ||
+      P.page_stride < (long long)p->page_size * hkv * d)
+    return fail(SA_ERR_INVALID_ARG, "a stride is shorter than its row or page");
+  P.k = static_cast<const __nv_bfloat16*>(k);
+  P.v = static_cast<const __nv_bfloat16*>(v);
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.slots = slots;
+  P.positions = positions;
+  P.kc = static_cast<__nv_bfloat16*>(k_cache);
+  P.vc = static_cast<__nv_bfloat16*>(v_cache);
+  P.qo = static_cast<__nv_bfloat16*>(q_out);
+  P.err = p->err ? p->err : default_error_word();
+  if (!P.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  P.T = p->tokens;
+  P.Hkv = hkv;
+  P.Hq = hq;
+  P.d = d;
+  P.page = p->page_size;
+  P.rows_end = p->num_pages * p->page_size;
+  P.rope = rope ? 1 : 0;
+  const int half = d / 2;
+  if (rope) {
+    const double inv_two_pi = 0.15915494309189533576888376337251;
+    for (int i = 0; i < half; ++i)
+      P.freq[i] = uint64_t(std::ldexp(std::pow(p->rope_base, -2.0 * i / d) * inv_two_pi, 64));
+  }
+  const bool vec = d % 16 == 0 && aligned(k, 16) && aligned(v, 16) && aligned(k_cache, 16) &&
+                   aligned(v_cache, 16) && (!with_q || (aligned(q, 16) && aligned(q_out, 16))) &&
+                   P.ks % 8 == 0 && P.vs % 8 == 0 && P.qs % 8 == 0 && P.page_stride % 8 == 0;
+  // enough tokens per block for kAppendPre items per thread, within its angle slots
+  const int per_tok = (2 * hkv + hq) * (vec ? half / 8 : half);
+  int tpb = (kAppendPre * kAppendThreads) / per_tok;
+  if (tpb * half > kMaxAngles) tpb = kMaxAngles / half;
+  // no fewer blocks than would fill the GPU
+  const int even = p->tokens / 304;
+  if (tpb > even) tpb = even;
+  P.tpb = tpb < 1 ? 1 : tpb;
+  const unsigned grid = unsigned((p->tokens + P.tpb - 1) / P.tpb);
+  if (vec)
+    sa_paged_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(P);
+  else
+    sa_paged_append_kernel<false><<<grid, kAppendThreads, 0, stream>>>(P);
+  const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "append launch: %s", cudaGetErrorString(ce));
+  return succeed();
+}
