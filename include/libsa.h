@@ -365,8 +365,7 @@ enum {
   SA_PAGED_AUTO = 0,  /* requests with few new rows on the row kernel, others on the tile kernel */
   SA_PAGED_ROWS = 1,  /* row kernel for every request: warps stream the keys of up to 16 query rows */
   SA_PAGED_TILES = 2  /* SWA: tcgen05 tiles of 256 query rows for every request;
-                         SA_ERR_UNSUPPORTED where they do not fit (num_q_heads / num_kv_heads
-                         must divide 32) */
+                         SA_ERR_UNSUPPORTED for more than 64 query heads per kv head */
 };
 
 /*

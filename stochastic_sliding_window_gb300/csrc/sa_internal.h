@@ -139,9 +139,17 @@ struct PagedProblem {
 // Row kernel (sa_paged_rows.cu).  Requests with more than row_limit new
 // tokens are skipped (swa path), or take their SWA term from swa_part, fp32
 // [T, Hq, d], gate applied (gated path).  `part`: the workspace.
-size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int sms);
+size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int row_limit, int sms);
 sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
                               const float* swa_part, void* part, int sms, cudaStream_t stream);
+
+// Tile kernel (sa_paged_tiles.cu): the SWA path of requests with more than
+// row_limit new tokens, into pb.out; with `gate` (logits [T, Hq]) as fp32
+// gated rows into part_out [T, Hq, d] instead.
+bool paged_tiles_supported(const PagedProblem& pb);
+size_t paged_tiles_workspace_bytes(const PagedProblem& pb, int sms);
+sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const float* gate,
+                               float* part_out, void* workspace, int sms, cudaStream_t stream);
 
 // sigma^{-1} kernels.
 sa_status_t launch_inverse_perm(const int32_t* perm, int32_t* inv, int batch, int n,

@@ -1,7 +1,7 @@
 // Serving over a paged K/V cache: the C-ABI entry points, the plan of a step
 // (block tables, slots and positions from the requests' lengths) and the
 // writer of new keys and values.  The attention itself is in
-// sa_paged_rows.cu.
+// sa_paged_rows.cu (few new tokens) and sa_paged_tiles.cu (many).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -412,8 +412,38 @@ static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
   return pb;
 }
 
-static size_t workspace_bytes(const PagedProblem& pb, Path path, int sms) {
-  return paged_rows_workspace_bytes(pb, path, sms);
+// Which kernels a call runs.  A request with n new tokens has n g query rows
+// per kv head; up to kRowLimit of them go to the row kernel, whose warps take
+// 16 rows over a run of keys, more to the tile kernel, whose blocks take 256.
+constexpr int kRowLimit = 64;
+
+struct Choice {
+  bool tiles, rows;
+  int row_limit;  // new tokens per request that the row kernel still takes
+};
+
+static Choice choose(const PagedProblem& pb, Path path, int kernel) {
+  Choice c{false, true, 0x7fffffff};
+  if (path == kPathSA || kernel == SA_PAGED_ROWS || !paged_tiles_supported(pb)) return c;
+  if (kernel == SA_PAGED_TILES) return Choice{true, false, 0};
+  const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
+  if (pb.max_new > limit) c = Choice{true, true, limit};
+  return c;
+}
+
+static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Workspace {
+  size_t rows, tiles, swa_part;  // parts, in this order
+  size_t total() const { return rows + tiles + swa_part; }
+};
+
+static Workspace workspace_parts(const PagedProblem& pb, Path path, const Choice& c, int sms) {
+  Workspace w{0, 0, 0};
+  if (c.rows) w.rows = round256(paged_rows_workspace_bytes(pb, path, c.row_limit, sms));
+  if (c.tiles) w.tiles = round256(paged_tiles_workspace_bytes(pb, sms));
+  if (c.tiles && path == kPathGated) w.swa_part = round256(size_t(pb.T) * pb.Hq * pb.d * 4);
+  return w;
 }
 
 static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, const void* k,
@@ -435,7 +465,11 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   const int sms = sm103_sms();
   if (sms == 0) return fail(SA_ERR_UNSUPPORTED, "device is not sm_103");
   PagedProblem pb = make_problem(prm, path);
-  const size_t need = workspace_bytes(pb, path, sms);
+  const Choice ch = choose(pb, path, prm->kernel);
+  if (prm->kernel == SA_PAGED_TILES && !ch.tiles)
+    return fail(SA_ERR_UNSUPPORTED, "the tile kernel takes at most 64 query heads per kv head");
+  const Workspace parts = workspace_parts(pb, path, ch, sms);
+  const size_t need = parts.total();
   if (need > 0 && (ws == nullptr || ws_bytes < need))
     return fail(SA_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
   if (need > 0 && !aligned(ws, 256))
@@ -450,9 +484,17 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   pb.out = out;
   pb.err = prm->err ? prm->err : default_error_word();
   if (!pb.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
-  if (prm->kernel == SA_PAGED_TILES) return fail(SA_ERR_UNSUPPORTED, "no tile kernel for this shape");
-  st = launch_paged_rows(pb, path, 0x7fffffff, nullptr, ws, sms, stream);
-  return st == SA_OK ? succeed() : st;
+  char* const w = static_cast<char*>(ws);
+  float* const swa_part = parts.swa_part ? reinterpret_cast<float*>(w + parts.rows + parts.tiles) : nullptr;
+  if (ch.tiles) {
+    st = launch_paged_tiles(pb, ch.row_limit, gate_swa, swa_part, w + parts.rows, sms, stream);
+    if (st != SA_OK) return st;
+  }
+  if (ch.rows) {
+    st = launch_paged_rows(pb, path, ch.row_limit, swa_part, w, sms, stream);
+    if (st != SA_OK) return st;
+  }
+  return succeed();
 }
 
 }  // namespace paged
@@ -492,7 +534,8 @@ extern "C" size_t sa_paged_workspace_size(const sa_paged_params_t* params, int32
   if (paged::check_sizes(params, pt) != SA_OK || params->tokens == 0) return 0;
   const int sms = paged::sm103_sms();
   if (sms == 0) return 0;
-  return paged::workspace_bytes(paged::make_problem(params, pt), pt, sms);
+  const PagedProblem pb = paged::make_problem(params, pt);
+  return paged::workspace_parts(pb, pt, paged::choose(pb, pt, params->kernel), sms).total();
 }
 
 extern "C" sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cached_lens,

@@ -644,20 +644,20 @@ struct Config {
   size_t part_bytes, desc_bytes;
 };
 
-static Config make_config(const PagedProblem& pb, Path path, int sms) {
+static Config make_config(const PagedProblem& pb, Path path, int row_limit, int sms) {
   Config c;
   c.rg = (pb.g + 15) / 16;
   // several tokens share a unit's 16 rows only where they share a window
-  c.tb = path == kPathSWA && pb.max_new > 1 && pb.g < 16 ? 16 / pb.g : 1;
-  if (c.tb > pb.max_new) c.tb = pb.max_new;
+  const int most_new = min(pb.max_new, row_limit);
+  c.tb = path == kPathSWA && pb.g < 16 ? min(16 / pb.g, most_new) : 1;
   c.R = c.rg > 1 ? 16 : c.tb * pb.g;
   c.slot_floats = (c.R * (pb.d + 2) + 3) / 4 * 4;  // 16-byte aligned slots
   const uint32_t pitch = uint32_t(pb.d) * 2 + 16;
   c.stage_bytes = (2 * kKeys + uint32_t(c.R)) * pitch + kMetaInts * 4;
   c.warp_bytes = c.stage_bytes * kStages;
   c.warps = int(kMaxSmem / c.warp_bytes);
-  const int most = pb.d == 128 ? 8 : 16;
-  if (c.warps > most) c.warps = most;
+  const int most_warps = pb.d == 128 ? 8 : 16;
+  if (c.warps > most_warps) c.warps = most_warps;
   c.workers = sms * c.warps;
   // Runs end at unit ends, without partials, where there are at least four
   // units per worker of at most 1024 keys each.
@@ -687,15 +687,15 @@ static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStr
 
 }  // namespace prow
 
-size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int sms) {
-  const prow::Config c = prow::make_config(pb, path, sms);
+size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int row_limit, int sms) {
+  const prow::Config c = prow::make_config(pb, path, row_limit, sms);
   return c.part_bytes + c.desc_bytes;
 }
 
 sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
                               const float* swa_part, void* part, int sms, cudaStream_t stream) {
   using namespace prow;
-  const Config c = make_config(pb, path, sms);
+  const Config c = make_config(pb, path, row_limit, sms);
   Params P;
   std::memset(&P, 0, sizeof(P));
   P.q = static_cast<const __nv_bfloat16*>(pb.q);

@@ -1,0 +1,956 @@
+// Tile kernel of the paged-cache attention: SWA (any window, full causal
+// among them) for requests that bring many new tokens, on the 5th-generation
+// tensor cores.
+//
+// Mathematics.  A tile is up to 256 query rows that share a kv head -- the g
+// query heads of Bt = floor(256 / g) consecutive new tokens, row r = t g + j
+// -- as two halves of M = 128.  Its keys, positions max(0, p_first - w + 1)
+// to p_last, are cut into chunks of 128.  One pass with an online softmax:
+//   S = Q K^T (TMEM),  P = 2^(scale log2(e) S - ref),  O += P V (TMEM),
+// where ref is the row's running maximum, raised (and O and the sum rescaled)
+// only when a chunk exceeds it by more than 2^8.  P is rounded to bf16, the
+// operand type of the second product; sums and O are fp32.
+//
+// What bounds it: the tensor cores, 4 d multiply-adds per row and key in two
+// MMAs of M = 128, N = 128 or d (128 cycles per 16 of K for N = 128).  So a
+// half's MMAs must run while the other half is in its softmax, and the
+// softmax of a half (128 rows x 128 keys) must take no longer than the other
+// half's two MMAs: one thread per row holds the row's 128 scores in
+// registers, one pass, masks only in the chunks that a window's end crosses.
+//
+// Split.  One block per SM.  All chunks of all tiles, laid end to end
+// (request, kv head, tile, chunk), are cut into equal runs, one per block, so
+// ragged batches balance; each block finds its run by a scan over the
+// requests' lengths.  Where tiles are long (32 chunks or more on average) a
+// run may end inside a tile: both parts leave fp32 partials in the workspace
+// and the join kernel merges them in order.  Else a tile belongs to the run
+// it starts in.
+//
+// Roles (12 warps, 168 registers per thread: a softmax thread holds 128 scores):
+//   warps 0-2   producers: resolve 128 keys per chunk through the block table,
+//               then cp.async the K and the V rows, zeros for keys there are
+//               none of; and each tile's Q rows
+//   warp 3      lane 0 issues every MMA; the warp owns TMEM
+//   warps 4-7   softmax and epilogue of rows 0-127, warps 8-11 of 128-255
+// TMEM (512 columns): S of half h in [128 h, +128), overwritten by its bf16 P
+// in the first 64 of them; O of half h in [256 + d h, +d).
+// Order of the MMAs: for each chunk c of a tile, for h = 0, 1: O_h += P_h V(c-1),
+// then S_h = Q_h K(c) -- one thread, one tensor pipe, which runs MMAs in the order
+// of their issue, so S_h may overwrite the P_h that the MMA before it reads.
+// Every wait is bounded (SA_ERRBIT_TIMEOUT).
+#include "sa_internal.h"
+#include "sa_tc_common.cuh"
+
+#include <cstring>
+
+namespace sa {
+namespace ptile {
+
+using namespace tcc;
+
+constexpr int kThreads = 384;
+constexpr int kProducers = 96;
+constexpr int kMmaWarp = 3;
+constexpr int kFirstSoftmaxWarp = 4;
+constexpr int kRows = 2 * kBM;
+constexpr int kKC = 128;            // keys per chunk
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kCutChunks = 32;      // tiles this long on average may be cut
+constexpr uint32_t kMaxSmem = 232448;
+
+struct Desc {  // per block: the tile that starts in its run and ends beyond it
+  int valid, c1, t0, rows, kvh, pad;
+};
+
+struct Params {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* seq_lens;
+  const float* gate;      // [T, Hq] logits: fp32 gated rows into part_out
+  __nv_bfloat16* out;
+  float* part_out;        // [T, Hq, D], with gate
+  float* part;            // partials [blocks][2][D/4][256] float4, then [blocks][2][256] (m, l)
+  Desc* desc;             // nullptr: tiles are never cut
+  int32_t* err;
+  long long q_stride, page_stride;
+  int B, T, max_new, row_limit, Hq, Hkv, g, Bt, page, num_pages, max_pages, w;
+  uint32_t off_k, off_v, off_key, off_bad, off_seg, off_bar;
+  float scale_log2;
+  long long timeout_cycles;
+};
+
+// Barriers (8 bytes each).  A phase is one use; chunks and tiles are counted
+// over the block's whole run.
+template <int NS>
+struct Bars {
+  enum : uint32_t {
+    kQfull = 0,           // Q rows of tile x landed (producers' copies)
+    kQfree = 1,           // the last S MMA of tile x done
+    kKfull = 2,           // [NS] K rows and key words of chunk c landed
+    kKfree = kKfull + NS, // [NS] both S MMAs of chunk c done
+    kVfull = kKfree + NS, // [NS]
+    kVfree = kVfull + NS, // [NS] both O MMAs of chunk c done
+    kSfull = kVfree + NS, // [h] S of the half's chunk c in TMEM
+    kPfull = kSfull + 2,  // [h] P of the half's chunk c written (4 warps)
+    kPVdone = kPfull + 2, // [h] the half's O MMA of chunk c done
+    kOfree = kPVdone + 2, // [h] the half's O of tile x read out (4 warps)
+    kDrain = kOfree + 2,
+    kNum = kDrain + 1,
+  };
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The same 32 bytes where the address is known to be 16-byte aligned only.
+__device__ __forceinline__ void st_global_2v4(void* p, const uint32_t (&r)[8]) {
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// ------------------------------------------------------------------ schedule
+
+// sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0: lattice points under a line,
+// counted by Euclid's descent -- take out the integer parts of slope and
+// offset, then exchange the axes.
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const long long t = a;
+    a = m;
+    m = t;
+  }
+  return s;
+}
+
+struct Request {
+  int q0, n, len;
+};
+__device__ __forceinline__ Request load_request(const Params& P, int b, bool report) {
+  Request r;
+  r.q0 = P.q_start[b];
+  const int q1 = P.q_start[b + 1];
+  r.len = P.seq_lens[b];
+  r.n = q1 - r.q0;
+  const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= P.T && r.n <= P.max_new && r.n <= r.len &&
+                  (long long)r.len <= (long long)P.max_pages * P.page;
+  if (!ok) {
+    if (report && q1 != r.q0) atomicOr(P.err, SA_ERRBIT_RANGE);
+    r.n = 0;
+  }
+  if (r.n <= P.row_limit) r.n = 0;
+  return r;
+}
+
+// First key and number of keys of tile `grp` of a request.
+__device__ __forceinline__ int tile_lo(const Params& P, const Request& r, int grp) {
+  return max(0, r.len - r.n + grp * P.Bt - P.w + 1);
+}
+__device__ __forceinline__ int tile_hi(const Params& P, const Request& r, int grp) {
+  return r.len - r.n + min(r.n, (grp + 1) * P.Bt);
+}
+__device__ __forceinline__ int tile_chunks(const Params& P, const Request& r, int grp) {
+  return (tile_hi(P, r, grp) - tile_lo(P, r, grp) + kKC - 1) / kKC;
+}
+__device__ __forceinline__ int num_tiles(const Params& P, const Request& r) {
+  return (r.n + P.Bt - 1) / P.Bt;
+}
+// Chunks of the request's first `k` tiles (of one kv head).
+__device__ __forceinline__ long long chunks_before(const Params& P, const Request& r, int k) {
+  const int nt = num_tiles(P, r);
+  long long s = 0;
+  if (k == nt && k > 0) {  // the last tile may be short
+    --k;
+    s = tile_chunks(P, r, k);
+  }
+  // tiles whose window reaches the first key: hi = c + (i + 1) Bt keys
+  const long long c = r.len - r.n;
+  const long long reach = (long long)P.w - 1 - c;  // largest first-token offset with lo = 0
+  long long ka = reach < 0 ? 0 : reach / P.Bt + 1;
+  if (ka > k) ka = k;
+  s += floor_sum(ka, kKC, P.Bt, c + P.Bt + kKC - 1);
+  s += (k - ka) * (((long long)P.Bt + P.w - 1 + kKC - 1) / kKC);
+  return s;
+}
+
+// A block's run of chunks and where it starts; found once by warp 0.
+struct Start {
+  long long begin, end, tile_off;  // tile_off: chunks of the first tile before `begin`
+  int b, kvh, grp, cut;
+};
+
+// One tile's part in the run.
+struct Seg {
+  Request r;
+  int b, kvh, grp;
+  int c0, c1, nch;  // chunks [c0, c1) of nch
+  long long pos;    // run position of chunk c0
+};
+
+// What the other roles need of it, in shared memory (slot: tile number mod 4).
+// Written before the tile's Qfull; a slot is written again four tiles on, when
+// the S MMAs of the third tile after it are done, which follow every softmax
+// warp's read of the second's.
+struct Shared {
+  int t0, nt, pos0, lo;  // first token's row, tokens, first position, first key
+  int kvh, c0, c1, nch;
+  int more;              // another tile part follows
+  int join;              // last block that holds a part of a tile cut here
+  int pad[2];
+};
+
+struct Cursor {
+  long long pos, end;
+  Request r;
+  int b, kvh, grp, off, cut, nt;
+  bool done;
+};
+__device__ __forceinline__ Cursor make_cursor(const Params& P, const Start& s) {
+  Cursor c;
+  c.pos = s.begin;
+  c.end = s.end;
+  c.b = s.b;
+  c.kvh = s.kvh;
+  c.grp = s.grp;
+  c.off = int(s.tile_off);
+  c.cut = s.cut;
+  c.done = s.begin >= s.end;
+  c.nt = 0;
+  if (!c.done) {
+    c.r = load_request(P, c.b, false);
+    c.nt = num_tiles(P, c.r);
+  }
+  return c;
+}
+__device__ __forceinline__ void next_tile(const Params& P, Cursor& c) {
+  c.off = 0;
+  if (++c.grp < c.nt) return;
+  c.grp = 0;
+  if (++c.kvh < P.Hkv) return;
+  c.kvh = 0;
+  do {
+    if (++c.b >= P.B) {
+      c.done = true;
+      return;
+    }
+    c.r = load_request(P, c.b, false);
+  } while (c.r.n == 0);
+  c.nt = num_tiles(P, c.r);
+}
+// The next tile part of the run; false at its end.
+__device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
+  if (c.done) return false;
+  if (!c.cut && c.off != 0) {  // the tile cut here is the previous block's
+    c.pos += tile_chunks(P, c.r, c.grp) - c.off;
+    next_tile(P, c);
+    if (c.done) return false;
+  }
+  if (c.pos >= c.end) return false;
+  s.r = c.r;
+  s.b = c.b;
+  s.kvh = c.kvh;
+  s.grp = c.grp;
+  s.nch = tile_chunks(P, c.r, c.grp);
+  s.c0 = c.off;
+  s.c1 = c.cut ? int(min((long long)s.nch, c.off + (c.end - c.pos))) : s.nch;
+  s.pos = c.pos;
+  c.pos += s.c1 - s.c0;
+  if (s.c1 == s.nch) {
+    next_tile(P, c);
+  } else {
+    c.done = true;  // the run ends inside this tile
+  }
+  return true;
+}
+
+// Warp 0: this block's run (collective over its lanes).
+__device__ Start find_start(const Params& P) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0, tiles = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    if (b0 + lane < P.B) {
+      const Request r = load_request(P, b0 + lane, blockIdx.x == 0);
+      if (r.n > 0) {
+        const int nt = num_tiles(P, r);
+        total += P.Hkv * chunks_before(P, r, nt);
+        tiles += (long long)P.Hkv * nt;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  Start s;
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  s.cut = P.desc != nullptr && total >= tiles * kCutChunks;
+  s.begin = per * blockIdx.x;
+  s.end = min(total, s.begin + per);
+  s.tile_off = 0;
+  s.b = s.kvh = s.grp = 0;
+  if (s.begin >= s.end) {
+    s.begin = s.end = 0;
+    return s;
+  }
+  long long before = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    long long x = 0;
+    if (b0 + lane < P.B) {
+      const Request r = load_request(P, b0 + lane, false);
+      if (r.n > 0) x = P.Hkv * chunks_before(P, r, num_tiles(P, r));
+    }
+    long long sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += a;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > s.begin);
+    if (hit != 0u) {
+      const int src = __ffs(hit) - 1;
+      s.b = b0 + src;
+      long long rel = s.begin - (before + __shfl_sync(0xffffffffu, sum - x, src));
+      const Request r = load_request(P, s.b, false);
+      const int nt = num_tiles(P, r);
+      const long long per_head = chunks_before(P, r, nt);
+      s.kvh = int(rel / per_head);
+      rel -= s.kvh * per_head;
+      int lo = 0, hi = nt - 1;  // the last tile that starts at or before rel
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (chunks_before(P, r, mid) <= rel) lo = mid; else hi = mid - 1;
+      }
+      s.grp = lo;
+      s.tile_off = rel - chunks_before(P, r, lo);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return s;
+}
+
+// ------------------------------------------------------------------ producers
+template <int D, int NS>
+__device__ void producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
+                              uint32_t bars, volatile int* abort_flag, volatile int* vote) {
+  using BR = Bars<NS>;
+  constexpr int CPR = D / 8;             // 16-byte chunks per row
+  constexpr int RPP = kProducers / CPR;  // rows per pass
+  constexpr uint32_t kTile = kKC * D * 2;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int cc = tid % CPR, r_first = tid / CPR;
+  const int kb = cc >> 3, c8 = cc & 7;
+  long long* skey = reinterpret_cast<long long*>(smem + P.off_key);    // [2][128] row offsets
+  uint32_t* sbad = reinterpret_cast<uint32_t*>(smem + P.off_bad);      // [4][4] keys of bad pages
+  int step = 0;
+  // every producer learns whether thread 0's wait succeeded; also orders
+  // their shared-memory writes before what follows
+  auto agree = [&](uint32_t bar, uint32_t parity, bool need) {
+    if (tid == 0)
+      vote[step & 1] = !need || bounded_wait(bar, parity, P.timeout_cycles, P.err, abort_flag) ? 1 : 0;
+    asm volatile("bar.sync 1, %0;" ::"n"(kProducers) : "memory");
+    const bool ok = vote[step & 1] != 0;
+    ++step;
+    return ok;
+  };
+  Cursor cur = make_cursor(P, start);
+  Seg s, ahead;
+  int n = 0, x = 0;  // chunks and tiles so far
+  bool ok = true;
+  bool more = next_seg(P, cur, ahead);
+  while (ok && more) {
+    s = ahead;
+    more = next_seg(P, cur, ahead);
+    const int lo = tile_lo(P, s.r, s.grp), hi = tile_hi(P, s.r, s.grp);
+    const int i0 = s.grp * P.Bt;
+    const int rows = min(P.Bt, s.r.n - i0) * P.g;
+    const int32_t* table = P.table + (long long)s.b * P.max_pages;
+    // page of key `at` of chunk c; -1: no key.  A thread resolves key tid, the
+    // first warp also key 96 + tid.
+    auto page_of = [&](int c, int at) {
+      const int j = lo + c * kKC + at;
+      return j < hi ? table[unsigned(j) / unsigned(P.page)] : -1;
+    };
+    int page = page_of(s.c0, tid), page2 = warp == 0 ? page_of(s.c0, kProducers + tid) : -1;
+    ok = agree(bars + 8 * BR::kQfree, uint32_t(x - 1) & 1u, x > 0);
+    if (!ok) break;
+    if (tid == 0) {
+      Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
+      sh->t0 = s.r.q0 + i0;
+      sh->nt = min(P.Bt, s.r.n - i0);
+      sh->pos0 = s.r.len - s.r.n + i0;
+      sh->lo = lo;
+      sh->kvh = s.kvh;
+      sh->c0 = s.c0;
+      sh->c1 = s.c1;
+      sh->nch = s.nch;
+      sh->more = more;
+      // a run that ends inside a tile is a full one
+      sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
+      mbar_arrive(bars + 8 * BR::kQfull);
+    }
+    for (int r = r_first; r < kRows; r += RPP) {
+      // rows past the last are zeros
+      const int rr = r < rows ? r : 0;
+      const int t = rr / P.g, j = rr - t * P.g;
+      cp_async16_zfill(sbase + uint32_t(r >> 7) * (kBM * D * 2) + kb * (kBM * 128) + (r & 127) * 128 +
+                           ((c8 ^ (r & 7)) << 4),
+                       P.q + (long long)(s.r.q0 + i0 + t) * P.q_stride + (s.kvh * P.g + j) * D + cc * 8,
+                       r < rows ? 16 : 0);
+    }
+    cp_async_arrive_noinc(bars + 8 * BR::kQfull);
+    for (int c = s.c0; c < s.c1; ++c, ++n) {
+      const int st = n % NS;
+      const uint32_t use = uint32_t(n / NS);
+      auto resolve = [&](int at, int pg) {
+        const int j = lo + c * kKC + at;
+        long long off = -1;
+        bool bad = false;
+        if (j < hi) {
+          if (unsigned(pg) < unsigned(P.num_pages)) {
+            const int in = int(unsigned(j) % unsigned(P.page));
+            off = (long long)pg * P.page_stride + ((long long)in * P.Hkv + s.kvh) * D;
+          } else {
+            bad = true;
+            atomicOr(P.err, SA_ERRBIT_RANGE);
+          }
+        }
+        skey[(n & 1) * kKC + at] = off;
+        const uint32_t word = __ballot_sync(0xffffffffu, bad);
+        if ((tid & 31) == 0) sbad[(n & 3) * 4 + (at >> 5)] = word;
+      };
+      resolve(tid, page);
+      if (warp == 0) resolve(kProducers + tid, page2);
+      if (c + 1 < s.c1) {
+        page = page_of(c + 1, tid);
+        if (warp == 0) page2 = page_of(c + 1, kProducers + tid);
+      }
+      ok = agree(bars + 8 * (BR::kKfree + st), (use - 1) & 1u, n >= NS);
+      if (!ok) break;
+      const long long* key = skey + (n & 1) * kKC;
+      const uint32_t sk = sbase + P.off_k + uint32_t(st) * kTile + kb * (kKC * 128);
+      const uint32_t sv = sbase + P.off_v + uint32_t(st) * kTile + kb * (kKC * 128);
+#pragma unroll 8
+      for (int i = r_first; i < kKC; i += RPP) {
+        const long long o = key[i];
+        cp_async16_zfill(sk + i * 128 + ((c8 ^ (i & 7)) << 4), P.k + (o >= 0 ? o : 0) + cc * 8, o >= 0 ? 16 : 0);
+      }
+      cp_async_arrive_noinc(bars + 8 * (BR::kKfull + st));
+      if (tid == 0) mbar_arrive(bars + 8 * (BR::kKfull + st));  // the key words
+      ok = agree(bars + 8 * (BR::kVfree + st), (use - 1) & 1u, n >= NS);
+      if (!ok) break;
+#pragma unroll 8
+      for (int i = r_first; i < kKC; i += RPP) {
+        const long long o = key[i];
+        cp_async16_zfill(sv + i * 128 + ((c8 ^ (i & 7)) << 4), P.v + (o >= 0 ? o : 0) + cc * 8, o >= 0 ? 16 : 0);
+      }
+      cp_async_arrive_noinc(bars + 8 * (BR::kVfull + st));
+    }
+    ++x;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // own copies land before exit
+}
+
+// ------------------------------------------------------------------ MMA issue
+template <int D, int NS>
+__device__ void mma_role(const Params& P, bool more, const Shared* seg, uint32_t sbase,
+                         uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
+  using BR = Bars<NS>;
+  constexpr uint32_t kTile = kKC * D * 2;
+  const uint32_t idesc_qk = idesc_bf16(kBM, kKC, 0), idesc_pv = idesc_bf16(kBM, D, 1);
+  const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + kBM * D * 2, 16, 1024)};
+  const uint64_t kd = sdesc_sw128(sbase + P.off_k, 16, 1024);
+  const uint64_t vd = sdesc_sw128(sbase + P.off_v, kKC * 128, 1024);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
+  };
+  // O_h (+)= P_h V of chunk number n, tile number x
+  auto pv = [&](int h, int n, int x, bool first) {
+    if (!wait(BR::kPfull + h, uint32_t(n))) return false;
+    if (h == 0 && !wait(BR::kVfull + n % NS, uint32_t(n / NS))) return false;
+    if (first && x > 0 && !wait(BR::kOfree + h, uint32_t(x - 1))) return false;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    const uint32_t o = tmem + uint32_t(2 * kKC + h * D), p = tmem + uint32_t(h * kKC);
+    uint64_t b = vd + uint64_t(n % NS) * (kTile / 16);
+#pragma unroll
+    for (int kk = 0; kk < kKC / 16; ++kk) {
+      umma_bf16_ts(o, p + 8 * kk, b, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      b += 128;  // 16 keys of 128 B
+    }
+    umma_commit(bars + 8 * (BR::kPVdone + h));
+    if (h == 1) umma_commit(bars + 8 * (BR::kVfree + n % NS));
+    return true;
+  };
+  auto qk = [&](int h, int n, bool last) {
+    fence_proxy_async_smem();  // cp.async (generic proxy) data -> tensor core reads
+    tc_fence_after();
+    const uint32_t d = tmem + uint32_t(h * kKC);
+    const uint64_t b0 = kd + uint64_t(n % NS) * (kTile / 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint64_t da = uint64_t((kk >> 2) * (kBM * 128 / 16) + (kk & 3) * 2);
+      const uint64_t db = uint64_t((kk >> 2) * (kKC * 128 / 16) + (kk & 3) * 2);
+      umma_bf16(d, qd[h] + da, b0 + db, idesc_qk, kk > 0 ? 1u : 0u);
+    }
+    umma_commit(bars + 8 * (BR::kSfull + h));
+    if (h == 1) {
+      umma_commit(bars + 8 * (BR::kKfree + n % NS));
+      if (last) umma_commit(bars + 8 * BR::kQfree);
+    }
+  };
+  int n = 0, x = 0;
+  bool ok = true;
+  for (; ok && more; ++x) {
+    if (!(ok = wait(BR::kQfull, uint32_t(x)))) break;
+    const Shared* sh = seg + (x & 3);
+    const int chunks = sh->c1 - sh->c0;
+    more = sh->more != 0;
+    for (int c = 0; ok && c < chunks; ++c, ++n) {
+      ok = wait(BR::kKfull + n % NS, uint32_t(n / NS));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (ok && c > 0) ok = pv(h, n - 1, x, c == 1);
+        if (ok) qk(h, n, c == chunks - 1);
+      }
+    }
+    // the last O MMAs do not wait for the next tile's operands
+    if (ok) ok = pv(0, n - 1, x, chunks == 1);
+    if (ok) ok = pv(1, n - 1, x, chunks == 1);
+  }
+  umma_commit(bars + 8 * BR::kDrain);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bars + 8 * BR::kDrain, 0) && clock64() - t0 < kDrainCycles) {
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+template <int D, int NS>
+__device__ void softmax_role(const Params& P, bool more, const Shared* seg, uint8_t* smem,
+                             uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
+  using BR = Bars<NS>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (warp - kFirstSoftmaxWarp) >> 2, quad = warp & 3;
+  const int row = h * kBM + quad * 32 + lane;
+  const int t = row / P.g, j = row - t * P.g;
+  const uint32_t lanes = uint32_t(quad * 32) << 16;
+  const uint32_t sb = tmem + lanes + uint32_t(h * kKC);
+  const uint32_t ob = tmem + lanes + uint32_t(2 * kKC + h * D);
+  const uint32_t* sbad = reinterpret_cast<const uint32_t*>(smem + P.off_bad);
+  auto wwait = [&](uint32_t bar, uint32_t parity) {
+    const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
+    return __all_sync(0xffffffffu, ok);
+  };
+  const uint64_t sl2 = f2_pack(P.scale_log2, P.scale_log2);
+  int n = 0, x = 0;
+  while (more) {
+    // the tile's first S also says that its entry in shared memory is there
+    if (!wwait(BR::kSfull + h, uint32_t(n))) return;
+    const Shared* sh = seg + (x & 3);
+    ++x;
+    more = sh->more != 0;
+    const int c0 = sh->c0, c1 = sh->c1;
+    const bool live = t < sh->nt;
+    const int pos = sh->pos0 + t;
+    // the row's keys as columns of chunk 0
+    const int khi = live ? pos - sh->lo : -1;
+    const int klo = max(0, pos - P.w + 1) - sh->lo;
+    const bool whole = c0 == 0 && c1 == sh->nch;
+    const int slot = int(blockIdx.x) * 2 + (c0 == 0 ? 1 : 0);
+    const size_t orow = live ? size_t(sh->t0 + t) * P.Hq + size_t(sh->kvh) * P.g + j : 0;
+    if (sh->join >= 0 && h == 0 && quad == 0 && lane == 0) {
+      Desc d;
+      d.valid = 1;
+      d.c1 = sh->join;
+      d.t0 = sh->t0;
+      d.rows = sh->nt * P.g;
+      d.kvh = sh->kvh;
+      d.pad = 0;
+      P.desc[blockIdx.x] = d;
+    }
+    float ref = -INFINITY, l = 0.f;
+    for (int c = c0; c < c1; ++c, ++n) {
+      if (c > c0 && !wwait(BR::kSfull + h, uint32_t(n))) return;
+      tc_fence_after();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32_async(sb + q * 32, v[q]);
+      const uint4 bad = *reinterpret_cast<const uint4*>(sbad + (n & 3) * 4);
+      const int lo = klo - c * kKC, hi = khi - c * kKC;
+      const bool clear = lo <= 0 && hi >= kKC - 1 && (bad.x | bad.y | bad.z | bad.w) == 0u;
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) reg_fence(v[q]);
+      if (!__all_sync(0xffffffffu, clear)) {
+        const uint32_t bw[4] = {bad.x, bad.y, bad.z, bad.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t keep = band_bits(lo, hi, q * 32) & ~bw[q];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((keep >> e) & 1u)) v[q][e] = __float_as_uint(-INFINITY);
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = __uint_as_float(v[q][0]);
+#pragma unroll
+        for (int e = 1; e + 1 < 32; e += 2)
+          mx[q] = fmax3(mx[q], __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+        mx[q] = fmaxf(mx[q], __uint_as_float(v[q][31]));
+      }
+      const float msc = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * P.scale_log2;
+      float alpha = 1.f;
+      bool rescale = false;
+      if (ref == -INFINITY) {
+        ref = msc;  // nothing attended before: O and l are still 0 for this row
+      } else if (msc > ref + kRescaleLog2) {
+        alpha = fast_exp2(ref - msc);
+        ref = msc;
+        l *= alpha;
+        rescale = true;
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+        // O must hold the O MMAs of every earlier chunk of the tile
+        if (!wwait(BR::kPVdone + h, uint32_t(n - 1))) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t o[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+              "%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]),
+                "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+              : "r"(ob + q * 16)
+              : "memory");
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st16(ob + q * 16, o);
+        }
+        tmem_wait_st();
+      }
+      const float nref = ref == -INFINITY ? 0.f : -ref;
+      const uint64_t nms = f2_pack(nref, nref);
+      uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = f2_unpack(f2_fma(
+              f2_pack(__uint_as_float(v[q][2 * e]), __uint_as_float(v[q][2 * e + 1])), sl2, nms));
+          const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+          acc[e & 1] = f2_add(acc[e & 1], f2_pack(p0, p1));
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(sb + q * 16, pk);
+      }
+      const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
+      l += (a0.x + a0.y) + (a1.x + a1.y);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (BR::kPfull + h));
+    }
+    // epilogue: the tile's part is done when its last O MMA is
+    if (!wwait(BR::kPVdone + h, uint32_t(n - 1))) return;
+    tc_fence_after();
+    float mul = l == 0.f ? 0.f : 1.f / l;
+    if (P.gate != nullptr && live) mul *= 1.f / (1.f + expf(-P.gate[orow]));
+    const uint64_t mul2 = f2_pack(mul, mul);
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      uint32_t o[32];
+      tmem_ld32(ob + q * 32, o);
+      if (q == D / 32 - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (BR::kOfree + h));
+      }
+      if (!whole) {
+        float4* dst = reinterpret_cast<float4*>(P.part) + (size_t(slot) * (D / 4) + q * 8) * kRows + row;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e * kRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+      } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), mul2));
+          o[2 * e] = __float_as_uint(y.x);
+          o[2 * e + 1] = __float_as_uint(y.y);
+        }
+        if (P.gate != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w[u] = o[8 * e + u];
+            st_global_v8(P.part_out + orow * D + q * 32 + e * 8, w);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              w[u] = pack_bf16x2(__uint_as_float(o[16 * e + 2 * u]), __uint_as_float(o[16 * e + 2 * u + 1]));
+            st_global_2v4(P.out + orow * D + q * 32 + e * 16, w);
+          }
+        }
+      }
+    }
+    if (!whole) {
+      float2* ml = reinterpret_cast<float2*>(P.part + size_t(gridDim.x) * 2 * kRows * D) + size_t(slot) * kRows + row;
+      *ml = make_float2(ref, l);
+    }
+  }
+}
+
+template <int D, int NS>
+__global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __grid_constant__ Params P) {
+  using BR = Bars<NS>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Start s_start;
+  __shared__ bool s_any;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + P.off_bar;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P.off_bar + 8 * BR::kNum);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 4);
+  volatile int* vote = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 8);  // [2]
+  const int warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const Start s = find_start(P);
+    Cursor cur = make_cursor(P, s);
+    Seg seg;
+    const bool any = next_seg(P, cur, seg);
+    if (threadIdx.x == 0) {
+      s_start = s;
+      s_any = any;
+    }
+  } else if (threadIdx.x == 32) {
+    mbar_init(bars + 8 * BR::kQfull, kProducers + 1);  // the copies, and the tile's entry
+    mbar_init(bars + 8 * BR::kQfree, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bars + 8 * (BR::kKfull + i), kProducers + 1);  // the copies, and the key words
+      mbar_init(bars + 8 * (BR::kKfree + i), 1);
+      mbar_init(bars + 8 * (BR::kVfull + i), kProducers);
+      mbar_init(bars + 8 * (BR::kVfree + i), 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(bars + 8 * (BR::kSfull + h), 1);
+      mbar_init(bars + 8 * (BR::kPfull + h), 4);
+      mbar_init(bars + 8 * (BR::kPVdone + h), 1);
+      mbar_init(bars + 8 * (BR::kOfree + h), 4);
+    }
+    mbar_init(bars + 8 * BR::kDrain, 1);
+    *abort_flag = 0;
+    if (P.desc != nullptr) P.desc[blockIdx.x].valid = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool any = s_any;
+  const Shared* seg = reinterpret_cast<const Shared*>(smem + P.off_seg);
+
+  if (warp >= kFirstSoftmaxWarp) {
+    softmax_role<D, NS>(P, any, seg, smem, tmem, bars, abort_flag);
+  } else if (warp < kMmaWarp) {
+    producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, vote);
+  } else {
+    if ((threadIdx.x & 31) == 0) mma_role<D, NS>(P, any, seg, sbase, tmem, bars, abort_flag);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+}
+
+// Joins the parts of each tile that the runs cut, in block order.  Block
+// (c, y) takes columns of the tile that starts in run c.
+template <int D>
+__global__ void __launch_bounds__(kRows) sa_paged_tiles_join_kernel(const __grid_constant__ Params P) {
+  const int c0 = blockIdx.x;
+  const Desc d = P.desc[c0];
+  if (!d.valid) return;
+  const int row = threadIdx.x, blocks = gridDim.x;
+  if (row >= d.rows) return;
+  const float2* ml = reinterpret_cast<const float2*>(P.part + size_t(blocks) * 2 * kRows * D);
+  auto slot = [&](int c) { return size_t(c * 2 + (c == c0 ? 1 : 0)); };
+  float m = -INFINITY;
+  for (int c = c0; c <= d.c1; ++c) m = fmaxf(m, ml[slot(c) * kRows + row].x);
+  float l = 0.f;
+  float4 a[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= d.c1; ++c) {
+    const float2 x = ml[slot(c) * kRows + row];
+    const float f = x.x == -INFINITY ? 0.f : fast_exp2(x.x - m);
+    l = fmaf(f, x.y, l);
+    const float4* src = reinterpret_cast<const float4*>(P.part) + (slot(c) * (D / 4) + blockIdx.y * 4) * kRows + row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = src[e * kRows];
+      a[e].x = fmaf(f, v.x, a[e].x);
+      a[e].y = fmaf(f, v.y, a[e].y);
+      a[e].z = fmaf(f, v.z, a[e].z);
+      a[e].w = fmaf(f, v.w, a[e].w);
+    }
+  }
+  const int t = row / P.g, j = row - t * P.g;
+  const size_t orow = size_t(d.t0 + t) * P.Hq + size_t(d.kvh) * P.g + j;
+  float s = l == 0.f ? 0.f : 1.f / l;
+  if (P.gate != nullptr) s *= 1.f / (1.f + expf(-P.gate[orow]));
+  const int col = blockIdx.y * 16;
+  if (P.gate != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(P.part_out + orow * D + col + 4 * e) =
+          make_float4(a[e].x * s, a[e].y * s, a[e].z * s, a[e].w * s);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[2 * e] = pack_bf16x2(a[e].x * s, a[e].y * s);
+      w[2 * e + 1] = pack_bf16x2(a[e].z * s, a[e].w * s);
+    }
+    st_global_2v4(P.out + orow * D + col, w);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+static bool may_cut(const PagedProblem& pb) {
+  const long long keys = min((long long)pb.window_swa + kRows, (long long)pb.max_pages * pb.page);
+  return keys >= (long long)kCutChunks * kKC;
+}
+
+template <int D, int NS>
+static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
+  const uint32_t tile = kKC * D * 2;
+  P.off_k = 2 * kBM * D * 2;
+  P.off_v = P.off_k + NS * tile;
+  P.off_key = P.off_v + NS * tile;
+  P.off_bad = P.off_key + 2 * kKC * 8;
+  P.off_seg = P.off_bad + 64;
+  P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared));
+  const uint32_t smem = P.off_bar + 8 * Bars<NS>::kNum + 16 + 1024;
+  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + 2 * kKC * 8 + 64 + 4 * sizeof(Shared) + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
+                    kMaxSmem, "shared memory");
+  cudaError_t ce = cudaFuncSetAttribute(sa_paged_tiles_kernel<D, NS>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (ce != cudaSuccess) return ce;
+  sa_paged_tiles_kernel<D, NS><<<sms, kThreads, smem, stream>>>(P);
+  if ((ce = cudaGetLastError()) != cudaSuccess || P.desc == nullptr) return ce;
+  sa_paged_tiles_join_kernel<D><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace ptile
+
+bool paged_tiles_supported(const PagedProblem& pb) {
+  return pb.g <= ptile::kRows / 4;
+}
+
+size_t paged_tiles_workspace_bytes(const PagedProblem& pb, int sms) {
+  if (!ptile::may_cut(pb)) return 0;
+  const size_t part = size_t(sms) * 2 * ptile::kRows * (pb.d + 2) * 4;
+  return (part + 255) / 256 * 256 + (size_t(sms) * sizeof(ptile::Desc) + 255) / 256 * 256;
+}
+
+sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const float* gate,
+                               float* part_out, void* workspace, int sms, cudaStream_t stream) {
+  using namespace ptile;
+  Params P;
+  std::memset(&P, 0, sizeof(P));
+  P.q = static_cast<const __nv_bfloat16*>(pb.q);
+  P.k = static_cast<const __nv_bfloat16*>(pb.k);
+  P.v = static_cast<const __nv_bfloat16*>(pb.v);
+  P.table = pb.table;
+  P.q_start = pb.q_start;
+  P.seq_lens = pb.seq_lens;
+  P.gate = gate;
+  P.out = static_cast<__nv_bfloat16*>(pb.out);
+  P.part_out = part_out;
+  if (may_cut(pb)) {
+    const size_t part = size_t(sms) * 2 * kRows * (pb.d + 2) * 4;
+    P.part = static_cast<float*>(workspace);
+    P.desc = reinterpret_cast<Desc*>(static_cast<char*>(workspace) + (part + 255) / 256 * 256);
+  }
+  P.err = pb.err;
+  P.q_stride = pb.q_stride;
+  P.page_stride = pb.page_stride;
+  P.B = pb.B;
+  P.T = pb.T;
+  P.max_new = pb.max_new;
+  P.row_limit = row_limit;
+  P.Hq = pb.Hq;
+  P.Hkv = pb.Hkv;
+  P.g = pb.g;
+  P.Bt = kRows / pb.g;
+  P.page = pb.page;
+  P.num_pages = pb.num_pages;
+  P.max_pages = pb.max_pages;
+  P.w = pb.window_swa;
+  P.scale_log2 = pb.scale * 1.4426950408889634f;
+  P.timeout_cycles = wait_limit_cycles();
+  const cudaError_t ce = pb.d == 128 ? launch_one<128, 2>(P, sms, stream) : launch_one<64, 4>(P, sms, stream);
+  if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged tile kernel launch: %s", cudaGetErrorString(ce));
+  return SA_OK;
+}
+
+}  // namespace sa

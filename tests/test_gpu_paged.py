@@ -42,6 +42,108 @@ def test_swa_rows(shape, window):
     b.check(out, "swa", window, what=shape)
 
 
+TILE_SHAPES = {
+    "one_row": ([1], [1], 1, 1, 64, 16),
+    "chunk_gqa": ([200, 1, 0, 65], [700, 300, 5, 65], 8, 2, 128, 16),
+    "chunk_mha": ([300, 257, 20], [300, 1000, 21], 2, 2, 64, 7),
+    "chunk_g5": ([90, 52], [130, 77], 10, 2, 128, 33),
+    "chunk_g64": ([9, 4], [40, 300], 64, 1, 64, 1),
+    "long": ([130], [9000], 8, 2, 128, 64),
+    "ragged": ([70, 3, 129, 1, 64, 500], [71, 3, 640, 2000, 64, 501], 8, 4, 64, 100),
+}
+
+
+@pytest.mark.parametrize("window", [1, 100, 129, 1000, ALL])
+@pytest.mark.parametrize("shape", TILE_SHAPES)
+def test_swa_tiles(shape, window):
+    new, total, hq, hkv, d, page = TILE_SHAPES[shape]
+    b = Batch(new, total, hq, hkv, d, page, seed=window % 97 + len(shape))
+    err = err_word()
+    out = b.run("swa", window, kernel=sa.PAGED_TILES, err=err)
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(out, "swa", window, weight_bits=8, what=shape)
+    assert torch.equal(out, b.run("swa", window, kernel=sa.PAGED_TILES, max_new=max(new)))
+
+
+@pytest.mark.parametrize("path", ["swa", "gated"])
+@pytest.mark.parametrize("shape", TILE_SHAPES)
+def test_auto_mixes_both_kernels(path, shape):
+    """Requests of few and of many new tokens in one call."""
+    new, total, hq, hkv, d, page = TILE_SHAPES[shape]
+    b = Batch(new, total, hq, hkv, d, page, seed=len(shape), perm_len=max(total), behind=3)
+    out = torch.full((b.t + 3, hq, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    err = err_word()
+    b.run(path, 90, 200, out=out, err=err)
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(out, path, 90, 200, weight_bits=8, what=shape)
+    assert (out[b.t:] == 2.0).all()
+
+
+def test_tiles_whose_reference_rises():
+    """Scores that grow along the keys by far more than 2^8 a chunk: O is
+    rescaled, and the first chunks' weights vanish."""
+    b = Batch([100], [1200], 4, 1, 128, 16, seed=3)
+    ramp = torch.linspace(0.05, 6.0, b.num_pages * 16, device="cuda").view(-1, 16, 1, 1)
+    b.q = b.args[0].abs()
+    order = torch.empty(b.num_pages, dtype=torch.long, device="cuda")
+    rest = np.setdiff1d(np.arange(b.num_pages), b.table[0])
+    order[torch.from_numpy(np.concatenate([b.table[0][b.table[0] >= 0], rest])).cuda()] = \
+        torch.arange(b.num_pages, device="cuda")
+    b.k = (b.k.abs() * ramp[order]).to(torch.bfloat16)
+    b.args = (b.q, b.k) + b.args[2:]
+    for kernel in (sa.PAGED_ROWS, sa.PAGED_TILES):
+        out = b.run("swa", ALL, kernel=kernel)
+        b.check(out, "swa", ALL, weight_bits=8, what=str(kernel))
+
+
+def test_tiles_with_bad_pages_and_lengths():
+    b = Batch([70, 80], [300, 400], 4, 2, 64, 16, seed=2)
+    table = b.table.copy()
+    table[0, 5] = -1
+    table[0, 18] = b.num_pages
+    args = list(b.args)
+    args[3] = i32(table)
+    b.args = tuple(args)
+    err = err_word()
+    out = b.run("swa", ALL, kernel=sa.PAGED_TILES, err=err)
+    assert sa.check_error(err) == sa.SA_ERR_BAD_PERM
+    assert torch.isfinite(out).all()
+    # the bad pages' keys are left out, as if the request had not had them
+    f = lambda x: x.float().cpu().numpy().astype(np.float64)
+    k, v = f(b.k), f(b.v)
+    j = np.array([x for x in range(300) if x // 16 not in (5, 18)])
+    kk, vv = k[table[0, j // 16], j % 16], v[table[0, j // 16], j % 16]
+    for i in (0, 33, 69):
+        live = j <= 230 + i
+        s = np.einsum("hgd,jhd->hgj", f(b.q)[i].reshape(2, 2, 64), kk[live]) / 8
+        p = np.exp(s - s.max(-1, keepdims=True))
+        y = np.einsum("hgj,jhd->hgd", p / p.sum(-1, keepdims=True), vv[live]).reshape(4, 64)
+        assert np.abs(f(out)[i] - y).max() < 0.03
+    err = err_word()
+    args[5] = i32([300, 79])
+    b.args = tuple(args)
+    out.fill_(6.0)
+    b.run("swa", ALL, kernel=sa.PAGED_TILES, err=err, out=out)
+    assert (out[70:] == 6.0).all() and sa.check_error(err) == sa.SA_ERR_BAD_PERM
+
+
+def test_tile_waits_give_up_within_their_bound():
+    """A wait limit far below a chunk's time: the call returns with the
+    timeout bit, the context stays usable."""
+    b = Batch([300], [3000], 8, 2, 128, 16, seed=1)
+    err = err_word()
+    sa.set_wait_limit(50)
+    try:
+        b.run("swa", ALL, kernel=sa.PAGED_TILES, err=err)
+        assert sa.check_error(err) == sa.SA_ERR_TIMEOUT
+    finally:
+        sa.set_wait_limit(0)
+    err = err_word()
+    out = b.run("swa", ALL, kernel=sa.PAGED_TILES, err=err)
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(out, "swa", ALL, weight_bits=8)
+
+
 @pytest.mark.parametrize("window", [1, 16, 129])
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("path", ["sa", "gated"])
@@ -92,7 +194,7 @@ def test_snapped_runs_of_many_units():
     total = [950, 333, 700, 1000]
     b = Batch(new, total, 16, 16, 64, 32, seed=8, perm_len=1000)
     b.check(b.run("sa", 20), "sa", 20, what="sa")
-    b.check(b.run("gated", 20, 13), "gated", 20, 13, what="gated")
+    b.check(b.run("gated", 20, 13, kernel=sa.PAGED_ROWS), "gated", 20, 13, what="gated")
     b.check(b.run("swa", 13, kernel=sa.PAGED_ROWS), "swa", 13, what="swa")
 
 
