@@ -80,6 +80,12 @@ bool chunk_supported(const Problem& pb, Path path);
 // entry point or the encoding fails).
 bool encode_row_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows);
 
+// Tensor map of a bf16 tensor of 2 to 4 dimensions (innermost first; strides
+// of the outer ones in bytes) for TMA copies of boxes with the 128-byte
+// swizzle; elements outside are read as zeros.
+bool encode_box_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box);
+
 // Backward pass (sa_bwd.cu).  One path (SA or SWA) per call: the dQ kernel
 // over query tiles (writes the rows' log2 normaliser and D, and the
 // gate-logit gradient when a gate is given), then the dK/dV kernel over

@@ -27,10 +27,10 @@
 // it starts in.
 //
 // Roles (12 warps, 168 registers per thread: a softmax thread holds 128 scores):
-//   warps 0-2   producers: resolve 128 keys per chunk through the block table,
-//               then cp.async the K and the V rows, zeros for keys there are
-//               none of; and each tile's Q rows
-//   warp 3      lane 0 issues every MMA; the warp owns TMEM
+//   warp 0      producer: TMA.  A lane takes a page of the chunk and loads its
+//               run of rows in boxes of 64, 16, 4 and 1 rows of 128 bytes; lane
+//               0 loads a tile's Q as one box per 64 columns
+//   warp 1      lane 0 issues every MMA; the warp owns TMEM
 //   warps 4-7   softmax and epilogue of rows 0-127, warps 8-11 of 128-255
 // TMEM (512 columns): S of half h in [128 h, +128), overwritten by its bf16 P
 // in the first 64 of them; O of half h in [256 + d h, +d).
@@ -49,8 +49,7 @@ namespace ptile {
 using namespace tcc;
 
 constexpr int kThreads = 384;
-constexpr int kProducers = 96;
-constexpr int kMmaWarp = 3;
+constexpr int kMmaWarp = 1;
 constexpr int kFirstSoftmaxWarp = 4;
 constexpr int kRows = 2 * kBM;
 constexpr int kKC = 128;            // keys per chunk
@@ -63,9 +62,8 @@ struct Desc {  // per block: the tile that starts in its run and ends beyond it
 };
 
 struct Params {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
+  CUtensorMap tq;           // q [T, Hq, D] in boxes of a tile's rows
+  CUtensorMap tk[4], tv[4]; // caches [pages, page, Hkv, D] in boxes of 4^i rows of a page
   const int32_t* table;
   const int32_t* q_start;
   const int32_t* seq_lens;
@@ -75,9 +73,8 @@ struct Params {
   float* part;            // partials [blocks][2][D/4][256] float4, then [blocks][2][256] (m, l)
   Desc* desc;             // nullptr: tiles are never cut
   int32_t* err;
-  long long q_stride, page_stride;
   int B, T, max_new, row_limit, Hq, Hkv, g, Bt, page, num_pages, max_pages, w;
-  uint32_t off_k, off_v, off_key, off_bad, off_seg, off_bar;
+  uint32_t off_k, off_v, off_bad, off_seg, off_bar;
   float scale_log2;
   long long timeout_cycles;
 };
@@ -87,9 +84,9 @@ struct Params {
 template <int NS>
 struct Bars {
   enum : uint32_t {
-    kQfull = 0,           // Q rows of tile x landed (producers' copies)
+    kQfull = 0,           // Q rows of tile x landed
     kQfree = 1,           // the last S MMA of tile x done
-    kKfull = 2,           // [NS] K rows and key words of chunk c landed
+    kKfull = 2,           // [NS] K rows of chunk c landed
     kKfree = kKfull + NS, // [NS] both S MMAs of chunk c done
     kVfull = kKfree + NS, // [NS]
     kVfree = kVfull + NS, // [NS] both O MMAs of chunk c done
@@ -102,8 +99,11 @@ struct Bars {
   };
 };
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -136,6 +136,14 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
 __device__ __forceinline__ void st_global_2v4(void* p, const uint32_t (&r)[8]) {
   reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
   reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+__device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
 
 // ------------------------------------------------------------------ schedule
@@ -367,52 +375,66 @@ __device__ Start find_start(const Params& P) {
   return s;
 }
 
-// ------------------------------------------------------------------ producers
+// ------------------------------------------------------------------ producer
+
+// What a chunk's consumers need beside its rows (slot: chunk number mod 8).
+// Its slot is written again for chunk n + 8, once the S MMAs of chunk n + 7 - NS
+// are done, NS <= 4: they follow every reading of chunk n's.
+constexpr int kKeySlots = 8;
+struct Keys {
+  uint32_t bad[4];  // bit j: key j of the chunk lies in a bad page
+  int good;         // some key of the tile part, up to this chunk, does not
+  int steps;        // 16-key steps that hold keys
+  int pad[2];
+};
+
+// A run of `len` rows of a page from row `in` to rows r .. of a stage, in
+// boxes of 64, 16, 4 and 1 rows; or `len` copies of one row.
+template <int D>
+__device__ __forceinline__ void load_run(const CUtensorMap* maps, uint32_t dst, int r, int len, int in,
+                                         int page, int kvh, bool same, uint32_t bar) {
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const int step = 1 << (2 * i);
+    if (same && i > 0) continue;
+    for (; len >= step; len -= step) {
+#pragma unroll
+      for (int kb = 0; kb < D / 64; ++kb)
+        tma_box4(dst + uint32_t(kb * (kKC * 128) + r * 128), maps + i, kb * 64, kvh, in, page, bar);
+      r += step;
+      if (!same) in += step;
+    }
+  }
+}
+
 template <int D, int NS>
 __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
-                              uint32_t bars, volatile int* abort_flag, volatile int* vote) {
+                              uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
-  constexpr int CPR = D / 8;             // 16-byte chunks per row
-  constexpr int RPP = kProducers / CPR;  // rows per pass
   constexpr uint32_t kTile = kKC * D * 2;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  const int cc = tid % CPR, r_first = tid / CPR;
-  const int kb = cc >> 3, c8 = cc & 7;
-  long long* skey = reinterpret_cast<long long*>(smem + P.off_key);    // [2][128] row offsets
-  uint32_t* sbad = reinterpret_cast<uint32_t*>(smem + P.off_bad);      // [4][4] keys of bad pages
-  int step = 0;
-  // every producer learns whether thread 0's wait succeeded; also orders
-  // their shared-memory writes before what follows
-  auto agree = [&](uint32_t bar, uint32_t parity, bool need) {
-    if (tid == 0)
-      vote[step & 1] = !need || bounded_wait(bar, parity, P.timeout_cycles, P.err, abort_flag) ? 1 : 0;
-    asm volatile("bar.sync 1, %0;" ::"n"(kProducers) : "memory");
-    const bool ok = vote[step & 1] != 0;
-    ++step;
-    return ok;
+  const int lane = threadIdx.x & 31;
+  auto wwait = [&](uint32_t bar, uint32_t parity) {
+    const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
+    return __all_sync(0xffffffffu, ok);
   };
   Cursor cur = make_cursor(P, start);
   Seg s, ahead;
-  int n = 0, x = 0;  // chunks and tiles so far
+  int n = 0, x = 0;             // chunks and tiles so far
+  int nq = 0, nk = 0, nv = 0;   // Q, K and V loads begun
   bool ok = true;
   bool more = next_seg(P, cur, ahead);
-  while (ok && more) {
+  for (; ok && more; ++x) {
     s = ahead;
     more = next_seg(P, cur, ahead);
     const int lo = tile_lo(P, s.r, s.grp), hi = tile_hi(P, s.r, s.grp);
     const int i0 = s.grp * P.Bt;
-    const int rows = min(P.Bt, s.r.n - i0) * P.g;
     const int32_t* table = P.table + (long long)s.b * P.max_pages;
-    // page of key `at` of chunk c; -1: no key.  A thread resolves key tid, the
-    // first warp also key 96 + tid.
-    auto page_of = [&](int c, int at) {
-      const int j = lo + c * kKC + at;
-      return j < hi ? table[unsigned(j) / unsigned(P.page)] : -1;
-    };
-    int page = page_of(s.c0, tid), page2 = warp == 0 ? page_of(s.c0, kProducers + tid) : -1;
-    ok = agree(bars + 8 * BR::kQfree, uint32_t(x - 1) & 1u, x > 0);
-    if (!ok) break;
-    if (tid == 0) {
+    // page of table column `col` (columns hi and on: not looked at)
+    const int last_col = int(unsigned(hi - 1) / unsigned(P.page));
+    auto page_at = [&](int col) { return col <= last_col ? table[col] : -1; };
+    int page = page_at(int(unsigned(lo + s.c0 * kKC) / unsigned(P.page)) + lane);
+    if (x > 0 && !(ok = wwait(BR::kQfree, uint32_t(x - 1)))) break;
+    if (lane == 0) {
       Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
       sh->t0 = s.r.q0 + i0;
       sh->nt = min(P.Bt, s.r.n - i0);
@@ -425,109 +447,159 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       sh->more = more;
       // a run that ends inside a tile is a full one
       sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
-      mbar_arrive(bars + 8 * BR::kQfull);
+      // rows of other tokens behind the tile's are computed and not written
+      mbar_arrive_expect_tx(bars + 8 * BR::kQfull, uint32_t(P.Bt * P.g) * D * 2);
+      for (int kb = 0; kb < D / 64; ++kb)
+        tma_box3(sbase + kb * (kRows * 128), &P.tq, kb * 64, s.kvh * P.g, s.r.q0 + i0, bars + 8 * BR::kQfull);
     }
-    for (int r = r_first; r < kRows; r += RPP) {
-      // rows past the last are zeros
-      const int rr = r < rows ? r : 0;
-      const int t = rr / P.g, j = rr - t * P.g;
-      cp_async16_zfill(sbase + uint32_t(r >> 7) * (kBM * D * 2) + kb * (kBM * 128) + (r & 127) * 128 +
-                           ((c8 ^ (r & 7)) << 4),
-                       P.q + (long long)(s.r.q0 + i0 + t) * P.q_stride + (s.kvh * P.g + j) * D + cc * 8,
-                       r < rows ? 16 : 0);
-    }
-    cp_async_arrive_noinc(bars + 8 * BR::kQfull);
+    ++nq;
+    // a good key's place, which stands in for keys of bad pages (whose weight is 0)
+    int gpage = 0, gin = 0;
+    bool good = false;
     for (int c = s.c0; c < s.c1; ++c, ++n) {
       const int st = n % NS;
-      const uint32_t use = uint32_t(n / NS);
-      auto resolve = [&](int at, int pg) {
-        const int j = lo + c * kKC + at;
-        long long off = -1;
-        bool bad = false;
-        if (j < hi) {
-          if (unsigned(pg) < unsigned(P.num_pages)) {
-            const int in = int(unsigned(j) % unsigned(P.page));
-            off = (long long)pg * P.page_stride + ((long long)in * P.Hkv + s.kvh) * D;
-          } else {
-            bad = true;
-            atomicOr(P.err, SA_ERRBIT_RANGE);
-          }
-        }
-        skey[(n & 1) * kKC + at] = off;
-        const uint32_t word = __ballot_sync(0xffffffffu, bad);
-        if ((tid & 31) == 0) sbad[(n & 3) * 4 + (at >> 5)] = word;
+      const int j0 = lo + c * kKC, j1 = min(hi, j0 + kKC);
+      const int col0 = int(unsigned(j0) / unsigned(P.page)), cols = int(unsigned(j1 - 1) / unsigned(P.page)) - col0 + 1;
+      // this lane's run of keys: those of table column col0 + i
+      auto run = [&](int i, int& r, int& len, int& in) {
+        const int a = max(j0, (col0 + i) * P.page);
+        r = a - j0;
+        len = min(j1 - a, P.page - (a - (col0 + i) * P.page));
+        in = a - (col0 + i) * P.page;
       };
-      resolve(tid, page);
-      if (warp == 0) resolve(kProducers + tid, page2);
-      if (c + 1 < s.c1) {
-        page = page_of(c + 1, tid);
-        if (warp == 0) page2 = page_of(c + 1, kProducers + tid);
+      // (pages of fewer than 5 tokens give some lanes more than one column)
+      uint32_t bad[4] = {0, 0, 0, 0};
+      bool any_bad = false;
+      int last_good = -1;
+      for (int i = lane; i < cols; i += 32) {
+        const int pg = i < 32 ? page : table[col0 + i];
+        if (unsigned(pg) < unsigned(P.num_pages)) {
+          last_good = i;
+        } else {
+          int r, len, in;
+          run(i, r, len, in);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) bad[w] |= band_bits(r, r + len - 1, w * 32);
+          any_bad = true;
+        }
       }
-      ok = agree(bars + 8 * (BR::kKfree + st), (use - 1) & 1u, n >= NS);
-      if (!ok) break;
-      const long long* key = skey + (n & 1) * kKC;
-      const uint32_t sk = sbase + P.off_k + uint32_t(st) * kTile + kb * (kKC * 128);
-      const uint32_t sv = sbase + P.off_v + uint32_t(st) * kTile + kb * (kKC * 128);
-#pragma unroll 8
-      for (int i = r_first; i < kKC; i += RPP) {
-        const long long o = key[i];
-        cp_async16_zfill(sk + i * 128 + ((c8 ^ (i & 7)) << 4), P.k + (o >= 0 ? o : 0) + cc * 8, o >= 0 ? 16 : 0);
+      const unsigned fine = __ballot_sync(0xffffffffu, last_good >= 0);
+      uint32_t words = 0;  // lanes 0-3: the chunk's bad keys
+      if (fine != 0u) {
+        const int src = 31 - __clz(int(fine));
+        const int i = __shfl_sync(0xffffffffu, last_good, src);
+        int r, len;
+        run(i, r, len, gin);
+        gpage = i < 32 ? __shfl_sync(0xffffffffu, page, i) : table[col0 + i];
+        good = true;
       }
-      cp_async_arrive_noinc(bars + 8 * (BR::kKfull + st));
-      if (tid == 0) mbar_arrive(bars + 8 * (BR::kKfull + st));  // the key words
-      ok = agree(bars + 8 * (BR::kVfree + st), (use - 1) & 1u, n >= NS);
-      if (!ok) break;
-#pragma unroll 8
-      for (int i = r_first; i < kKC; i += RPP) {
-        const long long o = key[i];
-        cp_async16_zfill(sv + i * 128 + ((c8 ^ (i & 7)) << 4), P.v + (o >= 0 ? o : 0) + cc * 8, o >= 0 ? 16 : 0);
+      if (__any_sync(0xffffffffu, any_bad)) {
+        if (any_bad) atomicOr(P.err, SA_ERRBIT_RANGE);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t v = __reduce_or_sync(0xffffffffu, bad[w]);
+          if (lane == w) words = v;
+        }
       }
-      cp_async_arrive_noinc(bars + 8 * (BR::kVfull + st));
+      Keys* keys = reinterpret_cast<Keys*>(smem + P.off_bad) + (n % kKeySlots);
+      const int steps = (j1 - j0 + 15) / 16, fill = steps * 16 - (j1 - j0);
+      if (lane < 4) keys->bad[lane] = words;
+      if (lane == 0) {
+        keys->good = good;
+        keys->steps = steps;
+      }
+      auto load = [&](const CUtensorMap* maps, uint32_t dst, uint32_t bar) {
+        for (int i = lane; i < cols; i += 32) {
+          const int pg = i < 32 ? page : table[col0 + i];
+          const bool ok_page = unsigned(pg) < unsigned(P.num_pages);
+          int r, len, in;
+          run(i, r, len, in);
+          load_run<D>(maps, dst, r, len, ok_page ? in : gin, ok_page ? pg : gpage, s.kvh, !ok_page, bar);
+        }
+      };
+      if (n >= NS && !(ok = wwait(BR::kKfree + st, uint32_t(n / NS - 1)))) break;
+      __syncwarp();
+      if (lane == 0)
+        mbar_arrive_expect_tx(bars + 8 * (BR::kKfull + st), uint32_t(j1 - j0) * D * 2);
+      __syncwarp();
+      // K rows past the last key keep what they held: their scores are masked
+      load(P.tk, sbase + P.off_k + uint32_t(st) * kTile, bars + 8 * (BR::kKfull + st));
+      ++nk;
+      if (n >= NS && !(ok = wwait(BR::kVfree + st, uint32_t(n / NS - 1)))) break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(bars + 8 * (BR::kVfull + st), uint32_t(steps * 16) * D * 2);
+      __syncwarp();
+      load(P.tv, sbase + P.off_v + uint32_t(st) * kTile, bars + 8 * (BR::kVfull + st));
+      // the last step's V rows past the last key: copies of a real row, since
+      // weights of 0 times what happens to be there need not be 0
+      if (lane < fill)
+        load_run<D>(P.tv, sbase + P.off_v + uint32_t(st) * kTile, j1 - j0 + lane, 1, gin, gpage, s.kvh, true,
+                    bars + 8 * (BR::kVfull + st));
+      ++nv;
+      if (c + 1 < s.c1) page = page_at(int(unsigned(j0 + kKC) / unsigned(P.page)) + lane);
     }
-    ++x;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");  // own copies land before exit
+  // A block must not exit with copies in flight (after a failed wait nobody
+  // else may be left to wait for them): each barrier's last use, bounded.
+  if (lane == 0) {
+    auto drain = [&](uint32_t bar, int uses) {
+      if (uses == 0) return;
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bars + 8 * bar, uint32_t(uses - 1) & 1u) && clock64() - t0 < kDrainCycles) {
+      }
+    };
+    drain(BR::kQfull, nq);
+    for (int i = 0; i < NS; ++i) {
+      drain(BR::kKfull + i, nk > i ? (nk - i + NS - 1) / NS : 0);
+      drain(BR::kVfull + i, nv > i ? (nv - i + NS - 1) / NS : 0);
+    }
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ MMA issue
 template <int D, int NS>
-__device__ void mma_role(const Params& P, bool more, const Shared* seg, uint32_t sbase,
-                         uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
+__device__ void mma_role(const Params& P, bool more, const Shared* seg, const Keys* keys,
+                         uint32_t sbase, uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
   const uint32_t idesc_qk = idesc_bf16(kBM, kKC, 0), idesc_pv = idesc_bf16(kBM, D, 1);
-  const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + kBM * D * 2, 16, 1024)};
+  // Q: column blocks of [256 rows x 128 B], half h from row 128 h
+  const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + kBM * 128, 16, 1024)};
   const uint64_t kd = sdesc_sw128(sbase + P.off_k, 16, 1024);
   const uint64_t vd = sdesc_sw128(sbase + P.off_v, kKC * 128, 1024);
   auto wait = [&](uint32_t bar, uint32_t parity) {
     return bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
   };
-  // O_h (+)= P_h V of chunk number n, tile number x
-  auto pv = [&](int h, int n, int x, bool first) {
+  // O_h (+)= P_h V of chunk number n, tile number x; add: O holds the sum of
+  // earlier chunks (one of whose keys, at least, is real: the V rows standing
+  // in for bad pages only may hold anything, and what they gave is dropped)
+  auto pv = [&](int h, int n, int x, bool first, bool add, int steps) {
     if (!wait(BR::kPfull + h, uint32_t(n))) return false;
     if (h == 0 && !wait(BR::kVfull + n % NS, uint32_t(n / NS))) return false;
     if (first && x > 0 && !wait(BR::kOfree + h, uint32_t(x - 1))) return false;
-    fence_proxy_async_smem();
     tc_fence_after();
     const uint32_t o = tmem + uint32_t(2 * kKC + h * D), p = tmem + uint32_t(h * kKC);
-    uint64_t b = vd + uint64_t(n % NS) * (kTile / 16);
+    const uint64_t b = vd + uint64_t(n % NS) * (kTile / 16);
+    if (steps == kKC / 16) {
 #pragma unroll
-    for (int kk = 0; kk < kKC / 16; ++kk) {
-      umma_bf16_ts(o, p + 8 * kk, b, idesc_pv, (!first || kk > 0) ? 1u : 0u);
-      b += 128;  // 16 keys of 128 B
+      for (int kk = 0; kk < kKC / 16; ++kk)
+        umma_bf16_ts(o, p + 8 * kk, b + 128 * kk, idesc_pv, (add || kk > 0) ? 1u : 0u);  // 16 keys of 128 B
+    } else {
+      for (int kk = 0; kk < steps; ++kk)
+        umma_bf16_ts(o, p + 8 * kk, b + 128 * kk, idesc_pv, (add || kk > 0) ? 1u : 0u);
     }
     umma_commit(bars + 8 * (BR::kPVdone + h));
     if (h == 1) umma_commit(bars + 8 * (BR::kVfree + n % NS));
     return true;
   };
   auto qk = [&](int h, int n, bool last) {
-    fence_proxy_async_smem();  // cp.async (generic proxy) data -> tensor core reads
     tc_fence_after();
     const uint32_t d = tmem + uint32_t(h * kKC);
     const uint64_t b0 = kd + uint64_t(n % NS) * (kTile / 16);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      const uint64_t da = uint64_t((kk >> 2) * (kBM * 128 / 16) + (kk & 3) * 2);
+      const uint64_t da = uint64_t((kk >> 2) * (kRows * 128 / 16) + (kk & 3) * 2);
       const uint64_t db = uint64_t((kk >> 2) * (kKC * 128 / 16) + (kk & 3) * 2);
       umma_bf16(d, qd[h] + da, b0 + db, idesc_qk, kk > 0 ? 1u : 0u);
     }
@@ -544,17 +616,20 @@ __device__ void mma_role(const Params& P, bool more, const Shared* seg, uint32_t
     const Shared* sh = seg + (x & 3);
     const int chunks = sh->c1 - sh->c0;
     more = sh->more != 0;
+    bool add = false;
     for (int c = 0; ok && c < chunks; ++c, ++n) {
       ok = wait(BR::kKfull + n % NS, uint32_t(n / NS));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (ok && c > 0) ok = pv(h, n - 1, x, c == 1);
+        if (ok && c > 0) ok = pv(h, n - 1, x, c == 1, add, kKC / 16);
         if (ok) qk(h, n, c == chunks - 1);
       }
+      if (c > 0) add = keys[(n - 1) % kKeySlots].good != 0;
     }
     // the last O MMAs do not wait for the next tile's operands
-    if (ok) ok = pv(0, n - 1, x, chunks == 1);
-    if (ok) ok = pv(1, n - 1, x, chunks == 1);
+    const int steps = keys[(n - 1) % kKeySlots].steps;  // (earlier chunks are full)
+    if (ok) ok = pv(0, n - 1, x, chunks == 1, add, steps);
+    if (ok) ok = pv(1, n - 1, x, chunks == 1, add, steps);
   }
   umma_commit(bars + 8 * BR::kDrain);
   const long long t0 = clock64();
@@ -564,7 +639,7 @@ __device__ void mma_role(const Params& P, bool more, const Shared* seg, uint32_t
 
 // ------------------------------------------------------------------ softmax
 template <int D, int NS>
-__device__ void softmax_role(const Params& P, bool more, const Shared* seg, uint8_t* smem,
+__device__ void softmax_role(const Params& P, bool more, const Shared* seg, const Keys* keys,
                              uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -574,7 +649,6 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, uint
   const uint32_t lanes = uint32_t(quad * 32) << 16;
   const uint32_t sb = tmem + lanes + uint32_t(h * kKC);
   const uint32_t ob = tmem + lanes + uint32_t(2 * kKC + h * D);
-  const uint32_t* sbad = reinterpret_cast<const uint32_t*>(smem + P.off_bad);
   auto wwait = [&](uint32_t bar, uint32_t parity) {
     const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
     return __all_sync(0xffffffffu, ok);
@@ -613,7 +687,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, uint
       uint32_t v[4][32];
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32_async(sb + q * 32, v[q]);
-      const uint4 bad = *reinterpret_cast<const uint4*>(sbad + (n & 3) * 4);
+      const uint4 bad = *reinterpret_cast<const uint4*>(keys[n % kKeySlots].bad);
       const int lo = klo - c * kKC, hi = khi - c * kKC;
       const bool clear = lo <= 0 && hi >= kKC - 1 && (bad.x | bad.y | bad.z | bad.w) == 0u;
       tmem_wait_ld();
@@ -703,6 +777,10 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, uint
     for (int q = 0; q < D / 32; ++q) {
       uint32_t o[32];
       tmem_ld32(ob + q * 32, o);
+      if (l == 0.f) {  // a row without keys is 0, whatever bad pages left in O
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
       if (q == D / 32 - 1) {
         tc_fence_before();
         __syncwarp();
@@ -759,7 +837,6 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   const uint32_t bars = sbase + P.off_bar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P.off_bar + 8 * BR::kNum);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 4);
-  volatile int* vote = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 8);  // [2]
   const int warp = threadIdx.x >> 5;
   if (warp == 0) {
     const Start s = find_start(P);
@@ -770,13 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
       s_start = s;
       s_any = any;
     }
-  } else if (threadIdx.x == 32) {
-    mbar_init(bars + 8 * BR::kQfull, kProducers + 1);  // the copies, and the tile's entry
+  } else if (threadIdx.x == 64) {
+    mbar_init(bars + 8 * BR::kQfull, 1);
     mbar_init(bars + 8 * BR::kQfree, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bars + 8 * (BR::kKfull + i), kProducers + 1);  // the copies, and the key words
+      mbar_init(bars + 8 * (BR::kKfull + i), 1);
       mbar_init(bars + 8 * (BR::kKfree + i), 1);
-      mbar_init(bars + 8 * (BR::kVfull + i), kProducers);
+      mbar_init(bars + 8 * (BR::kVfull + i), 1);
       mbar_init(bars + 8 * (BR::kVfree + i), 1);
     }
     for (int h = 0; h < 2; ++h) {
@@ -802,13 +879,14 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   const uint32_t tmem = *tmem_slot;
   const bool any = s_any;
   const Shared* seg = reinterpret_cast<const Shared*>(smem + P.off_seg);
+  const Keys* keys = reinterpret_cast<const Keys*>(smem + P.off_bad);
 
   if (warp >= kFirstSoftmaxWarp) {
-    softmax_role<D, NS>(P, any, seg, smem, tmem, bars, abort_flag);
-  } else if (warp < kMmaWarp) {
-    producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, vote);
-  } else {
-    if ((threadIdx.x & 31) == 0) mma_role<D, NS>(P, any, seg, sbase, tmem, bars, abort_flag);
+    softmax_role<D, NS>(P, any, seg, keys, tmem, bars, abort_flag);
+  } else if (warp == 0) {
+    producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag);
+  } else if (warp == kMmaWarp) {
+    if ((threadIdx.x & 31) == 0) mma_role<D, NS>(P, any, seg, keys, sbase, tmem, bars, abort_flag);
     __syncwarp();
   }
   tc_fence_before();
@@ -884,12 +962,11 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
   const uint32_t tile = kKC * D * 2;
   P.off_k = 2 * kBM * D * 2;
   P.off_v = P.off_k + NS * tile;
-  P.off_key = P.off_v + NS * tile;
-  P.off_bad = P.off_key + 2 * kKC * 8;
-  P.off_seg = P.off_bad + 64;
+  P.off_bad = P.off_v + NS * tile;
+  P.off_seg = P.off_bad + kKeySlots * uint32_t(sizeof(Keys));
   P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared));
   const uint32_t smem = P.off_bar + 8 * Bars<NS>::kNum + 16 + 1024;
-  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + 2 * kKC * 8 + 64 + 4 * sizeof(Shared) + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
+  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(Keys) + 4 * sizeof(Shared) + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
                     kMaxSmem, "shared memory");
   cudaError_t ce = cudaFuncSetAttribute(sa_paged_tiles_kernel<D, NS>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -903,7 +980,7 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
 }  // namespace ptile
 
 bool paged_tiles_supported(const PagedProblem& pb) {
-  return pb.g <= ptile::kRows / 4;
+  return pb.g <= ptile::kRows / 4;  // at least four tokens to a tile
 }
 
 size_t paged_tiles_workspace_bytes(const PagedProblem& pb, int sms) {
@@ -917,9 +994,18 @@ sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const floa
   using namespace ptile;
   Params P;
   std::memset(&P, 0, sizeof(P));
-  P.q = static_cast<const __nv_bfloat16*>(pb.q);
-  P.k = static_cast<const __nv_bfloat16*>(pb.k);
-  P.v = static_cast<const __nv_bfloat16*>(pb.v);
+  const uint64_t d2 = uint64_t(pb.d) * 2;
+  const uint64_t qdims[3] = {uint64_t(pb.d), uint64_t(pb.Hq), uint64_t(pb.T)};
+  const uint64_t qst[2] = {d2, uint64_t(pb.q_stride) * 2};
+  const uint32_t qbox[3] = {64, uint32_t(pb.g), uint32_t(kRows / pb.g)};
+  bool maps = encode_box_map(&P.tq, pb.q, 3, qdims, qst, qbox);
+  const uint64_t dims[4] = {uint64_t(pb.d), uint64_t(pb.Hkv), uint64_t(pb.page), uint64_t(pb.num_pages)};
+  const uint64_t st[3] = {d2, d2 * pb.Hkv, uint64_t(pb.page_stride) * 2};
+  for (int i = 0; i < 4 && maps; ++i) {
+    const uint32_t box[4] = {64, 1, 1u << (2 * i), 1};
+    maps = encode_box_map(&P.tk[i], pb.k, 4, dims, st, box) && encode_box_map(&P.tv[i], pb.v, 4, dims, st, box);
+  }
+  if (!maps) return fail(SA_ERR_CUDA, "paged tile kernel: cannot encode the tensor maps");
   P.table = pb.table;
   P.q_start = pb.q_start;
   P.seq_lens = pb.seq_lens;
@@ -932,8 +1018,6 @@ sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const floa
     P.desc = reinterpret_cast<Desc*>(static_cast<char*>(workspace) + (part + 255) / 256 * 256);
   }
   P.err = pb.err;
-  P.q_stride = pb.q_stride;
-  P.page_stride = pb.page_stride;
   P.B = pb.B;
   P.T = pb.T;
   P.max_new = pb.max_new;
