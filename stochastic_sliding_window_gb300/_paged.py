@@ -13,7 +13,7 @@ from ctypes import byref, c_double, c_float, c_int32, c_int64, c_void_p
 from typing import NamedTuple
 
 from . import _libsa
-from ._libsa import _check, _check_err, _need, _on_device, _shape
+from ._libsa import _check, _check_err, _need, _shape
 
 PAGED_AUTO, PAGED_ROWS, PAGED_TILES = 0, 1, 2
 _SWA, _SA, _GATED = 0, 1, 2
@@ -75,129 +75,149 @@ class PagedPlan(NamedTuple):
 
 
 class _On:
-    """The device of `t` made current for the calls inside, and the stream
-    they go to: the given one (made current too, so that what is allocated
-    inside belongs to it), else that device's current one."""
+    """The device numbered `index` made current for the calls inside, and the
+    stream they go to: the given one (made current too, so that what is
+    allocated inside belongs to it), else that device's current one."""
 
-    __slots__ = ("guards", "device")
+    __slots__ = ("guards", "index")
 
-    def __init__(self, t, stream):
+    def __init__(self, index, stream):
         import torch
-        self.device = t.device
-        self.guards = []
-        if t.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(t.device))
+        self.index = index
+        self.guards = ()
+        if index != torch.cuda.current_device():
+            self.guards = (torch.cuda.device(index),)
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-            elif stream.device != t.device:
-                raise ValueError(f"stream must be on {t.device}, got {stream.device}")
-            self.guards.append(torch.cuda.stream(stream))
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            elif stream.device.index != index:
+                raise ValueError(f"stream must be on cuda:{index}, got {stream.device}")
+            self.guards += (torch.cuda.stream(stream),)
 
     def __enter__(self):
         import torch
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
+def _rows(t, name, dtype, ndim):
+    """The shape of a contiguous tensor argument, its type and rank checked."""
+    try:
+        if t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+            return t.shape
+    except AttributeError:
+        pass
+    _need(t, name, dtype, ndim)  # says what is wrong
+
+
 def _tokens(t, name):
-    """bf16 [T, H, d] whose rows [H, d] are contiguous; returns the stride
-    between tokens."""
+    """bf16 [T, H, d] whose rows [H, d] are contiguous; returns its shape and
+    the stride between tokens."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
+    n, h, d = shape = t.shape
+    if t.is_contiguous():
+        return shape, h * d
     st = t.stride()
-    if n * h * d and ((st[2] != 1 and d > 1) or (st[1] != d and h > 1) or (st[0] < h * d and n > 1)):
+    if (st[2] != 1 and d > 1) or (st[1] != d and h > 1) or (st[0] < h * d and n > 1):
         raise ValueError(f"{name} must have contiguous [heads, head_dim] rows")
-    return st[0] if n > 1 else h * d
+    return shape, st[0] if n > 1 else h * d
 
 
 def _caches(k_cache, v_cache):
     """Both caches, bf16 [pages, page_size, Hkv, d], pages contiguous and the
-    same stride apart; returns that stride."""
+    same stride apart; returns their shape and that stride."""
     import torch
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        if t.dim() != 4 or 0 in t.shape:
-            raise ValueError(f"{name} must be [num_pages, page_size, Hkv, d], got {tuple(t.shape)}")
-    if k_cache.shape != v_cache.shape:
-        raise ValueError(f"v_cache must have shape {tuple(k_cache.shape)}, got {tuple(v_cache.shape)}")
-    n, ps, h, d = k_cache.shape
+    shape = k_cache.shape
+    if len(shape) != 4 or 0 in shape:
+        raise ValueError(f"k_cache must be [num_pages, page_size, Hkv, d], got {tuple(shape)}")
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache must have shape {tuple(shape)}, got {tuple(v_cache.shape)}")
+    n, ps, h, d = shape
     size = ps * h * d
+    if k_cache.is_contiguous() and v_cache.is_contiguous():
+        return shape, size
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         st = t.stride()
         if (st[3] != 1 and d > 1) or (st[2] != d and h > 1) or (st[1] != h * d and ps > 1) or \
                 (st[0] < size and n > 1):
             raise ValueError(f"{name} must have contiguous pages")
     if n == 1:
-        return size
+        return shape, size
     if k_cache.stride(0) != v_cache.stride(0):
         raise ValueError("v_cache must have its pages as far apart as k_cache")
-    return k_cache.stride(0)
+    return shape, k_cache.stride(0)
+
+
+def _one_device(first, name0, *named):
+    """The CUDA device number that all tensors share."""
+    index = first.get_device() if first.is_cuda else -1
+    if index < 0:
+        raise ValueError(f"{name0} must be a CUDA tensor")
+    for name, t in named:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+    return index
 
 
 def _forward(path, q, k_cache, v_cache, block_table, q_start, seq_lens, window, window_swa, max_new,
              softmax_scale, out, kernel, err, stream, perm=None, inv_perm=None, gate_sa=None,
              gate_swa=None):
     import torch
-    q_stride = _tokens(q, "q")
-    page_stride = _caches(k_cache, v_cache)
-    t, hq, d = q.shape
-    pages, page_size, hkv, dk = k_cache.shape
+    i32 = torch.int32
+    qshape, q_stride = _tokens(q, "q")
+    (pages, page_size, hkv, dk), page_stride = _caches(k_cache, v_cache)
+    t, hq, d = qshape
     if dk != d:
         raise ValueError(f"k_cache must have head_dim {d}, got {tuple(k_cache.shape)}")
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(q_start, "q_start", torch.int32, 1)
-    b = seq_lens.shape[0]
-    _shape(q_start, "q_start", (b + 1,))
-    if block_table.shape[0] != b:
+    rows, max_pages = _rows(block_table, "block_table", i32, 2)
+    b, = _rows(seq_lens, "seq_lens", i32, 1)
+    if _rows(q_start, "q_start", i32, 1)[0] != b + 1:
+        _shape(q_start, "q_start", (b + 1,))
+    if rows != b:
         raise ValueError(f"block_table must have {b} rows, got {tuple(block_table.shape)}")
-    named = [("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
-             ("q_start", q_start), ("seq_lens", seq_lens), ("err", err)]
     perm_rows = perm_len = 0
     if path != _SWA:
-        _need(perm, "perm", torch.int32, 2)
-        _need(inv_perm, "inv_perm", torch.int32, 2)
-        perm_rows, perm_len = perm.shape
+        perm_rows, perm_len = shape = _rows(perm, "perm", i32, 2)
         if perm_rows != b and perm_rows != 1:
             raise ValueError(f"perm must have {b} rows, or one for all, got {tuple(perm.shape)}")
-        _shape(inv_perm, "inv_perm", perm.shape)
-        named += [("perm", perm), ("inv_perm", inv_perm)]
+        if _rows(inv_perm, "inv_perm", i32, 2) != shape:
+            _shape(inv_perm, "inv_perm", shape)
     if path == _GATED:
         for name, g in (("gate_sa", gate_sa), ("gate_swa", gate_swa)):
-            _need(g, name, torch.float32, 2)
-            _shape(g, name, (t, hq))
-            named.append((name, g))
-    if out is not None:
-        _need(out, "out", torch.bfloat16, 3)
-        _shape(out, "out", q.shape)
-        named.append(("out", out))
-    _check_err(err)
-    _on_device(q, "q", named)
-    prm = SaPagedParams(b, t, int(max_new), hq, hkv, d, page_size, pages, block_table.shape[1],
-                        int(window), int(window_swa), perm_rows, perm_len, int(kernel),
-                        float(softmax_scale), 0, q_stride, page_stride, block_table.data_ptr(),
-                        q_start.data_ptr(), seq_lens.data_ptr(),
-                        err.data_ptr() if err is not None else None)
-    ref = byref(prm)
-    lib = _libsa.load()
-    with _On(q, stream) as s:
+            if tuple(_rows(g, name, torch.float32, 2)) != (t, hq):
+                _shape(g, name, (t, hq))
+    if out is not None and _rows(out, "out", torch.bfloat16, 3) != qshape:
+        _shape(out, "out", qshape)
+    if err is not None:
+        _check_err(err)
+    index = _one_device(q, "q", ("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
+                        ("q_start", q_start), ("seq_lens", seq_lens), ("perm", perm),
+                        ("inv_perm", inv_perm), ("gate_sa", gate_sa), ("gate_swa", gate_swa),
+                        ("out", out), ("err", err))
+    ref = byref(SaPagedParams(b, t, int(max_new), hq, hkv, d, page_size, pages, max_pages, int(window),
+                              int(window_swa), perm_rows, perm_len, int(kernel), float(softmax_scale), 0,
+                              q_stride, page_stride, block_table.data_ptr(), q_start.data_ptr(),
+                              seq_lens.data_ptr(), err.data_ptr() if err is not None else None))
+    lib = _libsa._lib or _libsa.load()
+    with _On(index, stream) as s:
         if out is None:
-            out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
         ws = lib.sa_paged_workspace_size(ref, path)
         work = torch.empty(ws, dtype=torch.uint8, device=q.device) if ws else None
         at = work.data_ptr() if ws else None
@@ -212,7 +232,8 @@ def _forward(path, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 
                                                 v_cache.data_ptr(), perm.data_ptr(),
                                                 inv_perm.data_ptr(), gate_sa.data_ptr(),
                                                 gate_swa.data_ptr(), out.data_ptr(), at, ws, s)
-    _check(st)
+    if st:
+        _check(st)
     return out
 
 
@@ -271,37 +292,40 @@ def paged_plan(new_lens, cached_lens, block_table, free_pages, num_free, page_si
     last token) and counts [3] = new tokens, pages taken, pages left.  If the
     step does not fit, nothing is planned and the error word says so."""
     import torch
-    for name, t in (("new_lens", new_lens), ("cached_lens", cached_lens),
-                    ("free_pages", free_pages), ("num_free", num_free)):
-        _need(t, name, torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    b = new_lens.shape[0]
-    _shape(cached_lens, "cached_lens", (b,))
-    if block_table.shape[0] != b:
+    i32 = torch.int32
+    b, = _rows(new_lens, "new_lens", i32, 1)
+    if _rows(cached_lens, "cached_lens", i32, 1)[0] != b:
+        _shape(cached_lens, "cached_lens", (b,))
+    rows, max_pages = _rows(block_table, "block_table", i32, 2)
+    if rows != b:
         raise ValueError(f"block_table must have {b} rows, got {tuple(block_table.shape)}")
-    _shape(num_free, "num_free", (1,))
+    free_capacity, = _rows(free_pages, "free_pages", i32, 1)
+    if _rows(num_free, "num_free", i32, 1)[0] != 1:
+        _shape(num_free, "num_free", (1,))
     n = int(max_tokens)
     if n < 0:
         raise ValueError("max_tokens must be >= 0")
-    _check_err(err)
-    given = [("q_start", q_start, b + 1), ("seq_lens", seq_lens, b), ("slots", slots, n),
-             ("positions", positions, n), ("counts", counts, 3)]
-    for name, t, size in given:
-        if t is not None:
-            _need(t, name, torch.int32, 1)
+    if err is not None:
+        _check_err(err)
+    outs = [q_start, seq_lens, slots, positions, counts]
+    names, sizes = ("q_start", "seq_lens", "slots", "positions", "counts"), [b + 1, b, n, n, 3]
+    for name, t, size in zip(names, outs, sizes):
+        if t is not None and _rows(t, name, i32, 1)[0] != size:
             _shape(t, name, (size,))
-    _on_device(new_lens, "new_lens", [("cached_lens", cached_lens), ("block_table", block_table),
-                                      ("free_pages", free_pages), ("num_free", num_free),
-                                      ("err", err)] + [(x[0], x[1]) for x in given])
-    ptr = lambda t: t.data_ptr() if t.numel() else None
-    with _On(new_lens, stream) as s:
-        outs = [torch.empty(size, dtype=torch.int32, device=new_lens.device) if t is None else t
-                for _, t, size in given]
-        st = _libsa.load().sa_paged_plan(
-            ptr(new_lens), ptr(cached_lens), b, ptr(block_table), block_table.shape[1],
-            ptr(free_pages), free_pages.shape[0], ptr(num_free), int(page_size), int(num_pages), n,
-            *[ptr(t) for t in outs], err.data_ptr() if err is not None else None, s)
-    _check(st)
+    index = _one_device(new_lens, "new_lens", ("cached_lens", cached_lens), ("block_table", block_table),
+                        ("free_pages", free_pages), ("num_free", num_free), ("err", err),
+                        *zip(names, outs))
+    lib = _libsa._lib or _libsa.load()
+    with _On(index, stream) as s:
+        if any(t is None for t in outs):  # what is not given, cut from one allocation
+            new = torch.empty(sum(sizes), dtype=i32, device=new_lens.device).split_with_sizes(sizes)
+            outs = [x if t is None else t for t, x in zip(outs, new)]
+        st = lib.sa_paged_plan(new_lens.data_ptr(), cached_lens.data_ptr(), b, block_table.data_ptr(),
+                               max_pages, free_pages.data_ptr(), free_capacity, num_free.data_ptr(),
+                               int(page_size), int(num_pages), n, *[t.data_ptr() for t in outs],
+                               err.data_ptr() if err is not None else None, s)
+    if st:
+        _check(st)
     return PagedPlan(*outs)
 
 
@@ -313,44 +337,48 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, rope_base: float
     [T]) as rope_ does, and q (bf16 [T, Hq, d]) is rotated into q_out, which
     is returned; otherwise None is."""
     import torch
-    ks, vs = _tokens(k, "k"), _tokens(v, "v")
-    page_stride = _caches(k_cache, v_cache)
-    t, hkv, d = k.shape
-    _shape(v, "v", k.shape)
-    pages, page_size, hc, dc = k_cache.shape
-    if (hc, dc) != (hkv, d):
+    (t, hkv, d), ks = _tokens(k, "k")
+    vshape, vs = _tokens(v, "v")
+    if vshape != k.shape:
+        _shape(v, "v", k.shape)
+    (pages, page_size, hc, dc), page_stride = _caches(k_cache, v_cache)
+    if hc != hkv or dc != d:
         raise ValueError(f"k_cache must be [num_pages, page_size, {hkv}, {d}], got {tuple(k_cache.shape)}")
-    _need(slots, "slots", torch.int32, 1)
-    _shape(slots, "slots", (t,))
-    rope = float(rope_base) != 0.0
+    if _rows(slots, "slots", torch.int32, 1)[0] != t:
+        _shape(slots, "slots", (t,))
+    rope_base = float(rope_base)
+    rope = rope_base != 0.0
     if positions is not None:
-        _need(positions, "positions", torch.int32, 1)
-        _shape(positions, "positions", (t,))
+        if _rows(positions, "positions", torch.int32, 1)[0] != t:
+            _shape(positions, "positions", (t,))
     elif rope:
         raise ValueError("positions are needed with rope_base")
     hq = qs = 0
     if q is not None:
         if not rope:
             raise ValueError("q is rotated only: it needs rope_base")
-        qs = _tokens(q, "q")
-        hq = q.shape[1]
-        _shape(q, "q", (t, hq, d))
-        if q_out is not None:
-            _need(q_out, "q_out", torch.bfloat16, 3)
-            _shape(q_out, "q_out", q.shape)
+        qshape, qs = _tokens(q, "q")
+        hq = qshape[1]
+        if qshape[0] != t or qshape[2] != d:
+            _shape(q, "q", (t, hq, d))
+        if q_out is not None and _rows(q_out, "q_out", torch.bfloat16, 3) != qshape:
+            _shape(q_out, "q_out", qshape)
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    _check_err(err)
-    _on_device(k, "k", [("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slots", slots),
-                        ("positions", positions), ("q", q), ("q_out", q_out), ("err", err)])
-    prm = SaPagedAppendParams(t, hkv, hq, d, page_size, pages, ks, vs, qs, page_stride,
-                              float(rope_base), err.data_ptr() if err is not None else None)
-    with _On(k, stream) as s:
+    if err is not None:
+        _check_err(err)
+    index = _one_device(k, "k", ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slots", slots),
+                        ("positions", positions), ("q", q), ("q_out", q_out), ("err", err))
+    ref = byref(SaPagedAppendParams(t, hkv, hq, d, page_size, pages, ks, vs, qs, page_stride, rope_base,
+                                    err.data_ptr() if err is not None else None))
+    lib = _libsa._lib or _libsa.load()
+    with _On(index, stream) as s:
         if q is not None and q_out is None:
             q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=k.device)
-        st = _libsa.load().sa_paged_append(
-            byref(prm), k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None,
-            slots.data_ptr(), positions.data_ptr() if rope else None, k_cache.data_ptr(),
-            v_cache.data_ptr(), q_out.data_ptr() if q is not None else None, s)
-    _check(st)
+        st = lib.sa_paged_append(ref, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None,
+                                 slots.data_ptr(), positions.data_ptr() if rope else None,
+                                 k_cache.data_ptr(), v_cache.data_ptr(),
+                                 q_out.data_ptr() if q is not None else None, s)
+    if st:
+        _check(st)
     return q_out

@@ -44,6 +44,34 @@ int32_t* default_error_word() {
   return static_cast<int32_t*>(p);
 }
 
+bool device_info(DeviceInfo* info) {
+  constexpr int kMost = 64;
+  static std::atomic<int32_t*> words[kMost];  // set last: its slot is complete
+  static std::atomic<int> sms[kMost];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  info->id = dev;
+  if (dev < kMost) {
+    if (int32_t* w = words[dev].load(std::memory_order_acquire)) {
+      info->sms = sms[dev].load(std::memory_order_relaxed);
+      info->error_word = w;
+      return true;
+    }
+  }
+  int major = 0, minor = 0, count = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+  info->sms = major == 10 && minor == 3 ? count : 0;
+  info->error_word = default_error_word();
+  if (info->error_word == nullptr) return false;
+  if (dev < kMost) {
+    sms[dev].store(info->sms, std::memory_order_relaxed);
+    words[dev].store(info->error_word, std::memory_order_release);
+  }
+  return true;
+}
+
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shared shape checks of the three forward calls.

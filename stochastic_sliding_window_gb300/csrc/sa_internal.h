@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "libsa.h"
 
 namespace sa {
@@ -118,6 +120,29 @@ sa_status_t launch_gate_projection(const void* x, int tokens, int d_model, int h
                                    float* a_sa, float* a_swa, int32_t* err, cudaStream_t stream);
 sa_status_t launch_rope(void* x, int batch, int n, int heads, int head_dim, double base,
                         cudaStream_t stream);
+
+// The current device, and what the serving calls ask of it: its SM count (0
+// unless it is an sm_103) and the library's error word there.  Looked up once
+// per device; the runtime calls would take longer than a small launch.
+struct DeviceInfo {
+  int id, sms;
+  int32_t* error_word;
+};
+bool device_info(DeviceInfo* info);
+
+// Lets a kernel take `bytes` of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(uint32_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce != cudaSuccess) return ce;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  ce = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (ce == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return ce;
+}
 
 // Attention over a paged cache, already validated on the host.
 struct PagedProblem {

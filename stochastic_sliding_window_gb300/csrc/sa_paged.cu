@@ -341,17 +341,6 @@ __global__ void __launch_bounds__(kAppendThreads) sa_paged_append_kernel(const _
 
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// SM count of the current device, 0 unless it is an sm_103.
-static int sm103_sms() {
-  int dev = 0, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return 0;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 static sa_status_t check_sizes(const sa_paged_params_t* p, Path path) {
   if (p == nullptr) return fail(SA_ERR_INVALID_ARG, "params is NULL");
   if (p->batch < 1 || p->tokens < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1)
@@ -462,7 +451,9 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
     return fail(SA_ERR_INVALID_ARG, "q, the caches and out must be 16-byte aligned");
   if (out == q || out == k || out == v) return fail(SA_ERR_INVALID_ARG, "out aliases an input");
-  const int sms = sm103_sms();
+  DeviceInfo dev;
+  if (!device_info(&dev)) return fail(SA_ERR_CUDA, "cannot resolve the current device and its error word");
+  const int sms = dev.sms;
   if (sms == 0) return fail(SA_ERR_UNSUPPORTED, "device is not sm_103");
   PagedProblem pb = make_problem(prm, path);
   const Choice ch = choose(pb, path, prm->kernel);
@@ -482,8 +473,7 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   pb.gate_sa = gate_sa;
   pb.gate_swa = gate_swa;
   pb.out = out;
-  pb.err = prm->err ? prm->err : default_error_word();
-  if (!pb.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  pb.err = prm->err ? prm->err : dev.error_word;
   char* const w = static_cast<char*>(ws);
   float* const swa_part = parts.swa_part ? reinterpret_cast<float*>(w + parts.rows + parts.tiles) : nullptr;
   if (ch.tiles) {
@@ -532,8 +522,9 @@ extern "C" size_t sa_paged_workspace_size(const sa_paged_params_t* params, int32
   if (path < 0 || path > 2) return 0;
   const Path pt = path == 0 ? kPathSWA : path == 1 ? kPathSA : kPathGated;
   if (paged::check_sizes(params, pt) != SA_OK || params->tokens == 0) return 0;
-  const int sms = paged::sm103_sms();
-  if (sms == 0) return 0;
+  DeviceInfo dev;
+  if (!device_info(&dev) || dev.sms == 0) return 0;
+  const int sms = dev.sms;
   const PagedProblem pb = paged::make_problem(params, pt);
   return paged::workspace_parts(pb, pt, paged::choose(pb, pt, params->kernel), sms).total();
 }
@@ -569,8 +560,9 @@ extern "C" sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cac
   P.slots = slots;
   P.positions = positions;
   P.counts = counts;
-  P.err = d_err ? d_err : default_error_word();
-  if (!P.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  DeviceInfo dev;
+  if (!device_info(&dev)) return fail(SA_ERR_CUDA, "cannot resolve the current device and its error word");
+  P.err = d_err ? d_err : dev.error_word;
   P.B = batch;
   P.max_pages = max_pages;
   P.free_capacity = free_capacity;
@@ -627,8 +619,9 @@ extern "C" sa_status_t sa_paged_append(const sa_paged_append_params_t* p, const 
   P.kc = static_cast<__nv_bfloat16*>(k_cache);
   P.vc = static_cast<__nv_bfloat16*>(v_cache);
   P.qo = static_cast<__nv_bfloat16*>(q_out);
-  P.err = p->err ? p->err : default_error_word();
-  if (!P.err) return fail(SA_ERR_CUDA, "cannot resolve the library error word");
+  DeviceInfo dev;
+  if (!device_info(&dev)) return fail(SA_ERR_CUDA, "cannot resolve the current device and its error word");
+  P.err = p->err ? p->err : dev.error_word;
   P.T = p->tokens;
   P.Hkv = hkv;
   P.Hq = hq;

@@ -19,9 +19,11 @@
 // whatever the lengths are and the host needs to know none.  A warp works
 // alone -- its own ring of cp.async stages, no block barriers -- and its
 // loads run ahead across the ends of units.  A unit cut by a run's end leaves
-// fp32 partial (O, m, l) in the workspace; the second kernel joins them in
-// worker order, so results do not depend on timing.  Where there are several
-// units per worker the runs end at unit ends instead and one launch does all.
+// fp32 partials (O, m, l) in the workspace, which are joined in worker order,
+// so results do not depend on timing: by the second kernel where runs are cut
+// over the whole GPU (long keys), by the block itself where a unit stays in
+// one block (windows of up to about a thousand keys); with several such units
+// per worker a unit is left to one warp and there is nothing to join.
 #include "sa_internal.h"
 #include "sa_tc_common.cuh"
 
@@ -47,11 +49,20 @@ enum : int {
   kAny = 64,      // some key of the tile is loaded
   kAddSwa = 128,  // gated: the SWA term comes from swa_part
   kNone = 256,    // no tile: the run is done
+  kRaw = 512,     // (this lane) the key is an entry of sigma not yet looked at
 };
 
 struct Desc {  // one per worker: the unit that starts in its run and ends beyond it
-  int valid, c1, t0, hr, nrows, tsa, tsw, add_swa;
-  long long u0, per;
+  int valid, t0, hr, nrows, tsa, tsw, add_swa, first;
+  long long u0, origin, per;  // tile x lies in the run of worker first + (x - origin) / per
+};
+
+// How the tiles are cut into runs.
+enum : int {
+  kCut = 0,     // equal runs, cut anywhere; the join kernel merges the parts
+  kWarps = 1,   // a unit belongs to the run it starts in: nothing to merge
+  kBlocks = 2,  // a unit belongs to the block whose run it starts in; the
+                // block's warps cut their share anywhere and merge it themselves
 };
 
 struct Params {
@@ -75,7 +86,7 @@ struct Params {
   int w, half, perm_len;
   int tb, rg, R;          // tokens and rows of a unit; row groups of a kv head (g > 16)
   int slot_floats;        // one partial: O [R, D], then (m, l) [R]; a multiple of 4
-  int workers, min_tiles, snap;
+  int warps, workers, min_tiles, mode;
   uint32_t stage_bytes, warp_bytes;
   float scale_log2;
 };
@@ -129,77 +140,131 @@ __device__ __forceinline__ Request load_request(const Params& P, int b, bool rep
   return r;
 }
 
+// Where a position of the laid-out tiles lies: request, its fields, and the
+// position's offset in the request's tiles.  All lanes of a warp call it.
+struct Place {
+  int b;
+  Request r;
+  long long off;
+};
+
+// The lengths of up to 32 requests, one per lane, and the sum of their tiles.
+struct Scan {
+  Request r;
+  long long x, sum;  // tiles of this lane's request; inclusive sum over the lanes
+};
+template <int PATH>
+__device__ __forceinline__ Scan scan32(const Params& P, int b0, int HR, bool report) {
+  const int lane = threadIdx.x & 31;
+  Scan s;
+  s.x = 0;
+  s.r = Request{0, 0, 0, 0, 0, 0};
+  if (b0 + lane < P.B) {
+    s.r = load_request<PATH>(P, b0 + lane, report);
+    s.x = (long long)s.r.groups * HR * (s.r.tsa + s.r.tsw);
+  }
+  s.sum = s.x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, s.sum, o);
+    if (lane >= o) s.sum += a;
+  }
+  return s;
+}
+
+// pos is below the sum of all tiles; `head` is the scan of the first 32.
+template <int PATH>
+__device__ __forceinline__ Place locate(const Params& P, const Scan& head, int HR, long long pos) {
+  Scan s = head;
+  long long before = 0;
+  Place p;
+  for (int b0 = 0;; b0 += 32) {
+    if (b0 > 0) s = scan32<PATH>(P, b0, HR, false);
+    const unsigned hit = __ballot_sync(0xffffffffu, before + s.sum > pos);
+    if (hit != 0u || b0 + 32 >= P.B) {
+      const int src = hit != 0u ? __ffs(hit) - 1 : 0;
+      p.b = b0 + src;
+      p.off = pos - (before + __shfl_sync(0xffffffffu, s.sum - s.x, src));
+      p.r.q0 = __shfl_sync(0xffffffffu, s.r.q0, src);
+      p.r.n = __shfl_sync(0xffffffffu, s.r.n, src);
+      p.r.len = __shfl_sync(0xffffffffu, s.r.len, src);
+      p.r.tsa = __shfl_sync(0xffffffffu, s.r.tsa, src);
+      p.r.tsw = __shfl_sync(0xffffffffu, s.r.tsw, src);
+      p.r.groups = __shfl_sync(0xffffffffu, s.r.groups, src);
+      return p;
+    }
+    before += __shfl_sync(0xffffffffu, s.sum, 31);
+  }
+}
+
+// The first unit start at or after pos.
+template <int PATH>
+__device__ __forceinline__ long long unit_from(const Params& P, const Scan& head, int HR, long long pos,
+                                               long long total) {
+  if (pos >= total) return total;
+  const Place p = locate<PATH>(P, head, HR, pos);
+  const int per_unit = p.r.tsa + p.r.tsw;
+  const int in = int(p.off % per_unit);
+  return in == 0 ? pos : pos + per_unit - in;
+}
+
+// One warp's run of tiles.
 template <int D, int PATH>
-__global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
   constexpr int kPitch = D * 2 + 16;  // 16 bytes over: eight rows of a matrix hit all banks
   constexpr int kCpr = D / 8;         // 16-byte chunks per row
   constexpr uint32_t kOffV = kKeys * kPitch, kOffQ = 2 * kKeys * kPitch;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int worker = warp * int(gridDim.x) + int(blockIdx.x);
-  if (worker >= P.workers) return;
-  uint8_t* ring = smem_raw + size_t(warp) * P.warp_bytes;
+  // runs that follow each other on different SMs, or in one block
+  const int worker = P.mode == kBlocks ? int(blockIdx.x) * P.warps + warp : warp * int(gridDim.x) + int(blockIdx.x);
+  uint8_t* ring = smem + size_t(warp) * P.warp_bytes;
   const uint32_t sring = smem_u32(ring);
   const uint32_t off_meta = kOffQ + uint32_t(P.R) * kPitch;
   const int HR = P.Hkv * P.rg;
 
-  // ---- this worker's run of tiles: [begin, end) of all units' tiles
-  long long total = 0, mine_sum = 0;
-  {
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-      const int b = b0 + lane;
-      if (b < P.B) {
-        const Request r = load_request<PATH>(P, b, worker == 0);
-        mine_sum += (long long)r.groups * HR * (r.tsa + r.tsw);
-      }
+  // ---- this worker's run [begin, end) of all units' tiles
+  const Scan head = scan32<PATH>(P, 0, HR, worker == 0);
+  long long total = __shfl_sync(0xffffffffu, head.sum, 31);
+  if (P.B > 32) {
+    long long more = 0;
+    for (int b = 32 + lane; b < P.B; b += 32) {
+      const Request r = load_request<PATH>(P, b, worker == 0);
+      more += (long long)r.groups * HR * (r.tsa + r.tsw);
     }
-    total = mine_sum;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+    total += more;
   }
-  long long per = (total + P.workers - 1) / P.workers;
-  if (per < P.min_tiles) per = P.min_tiles;
-  const long long begin = per * worker;
-  const long long end = min(total, begin + per);
+  long long origin = 0, limit = total, per;
+  int first = 0;
+  if (P.mode == kBlocks) {
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    first = int(blockIdx.x) * P.warps;
+    origin = unit_from<PATH>(P, head, HR, share * blockIdx.x, total);
+    limit = unit_from<PATH>(P, head, HR, share * (blockIdx.x + 1), total);
+    per = max((limit - origin + P.warps - 1) / P.warps, (long long)P.min_tiles);
+  } else {
+    per = max((total + P.workers - 1) / P.workers, (long long)P.min_tiles);
+  }
+  const bool snap = P.mode == kWarps;
+  const long long begin = origin + per * (worker - first);
+  const long long end = min(limit, begin + per);
   if (P.desc != nullptr && lane == 0) P.desc[worker].valid = 0;
-  if (begin >= total) return;
+  if (begin >= limit) return;
 
   // ---- cursor: request, group, head and tile of the next tile to fetch
-  int cb = 0;
+  int cb, cgrp, chr_, ctile;
   Request cr;
   long long cpos = begin;
-  int cgrp = 0, chr_ = 0, ctile = 0;
   {
-    long long before = 0;  // tiles of the requests before this chunk of 32
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-      const int b = b0 + lane;
-      long long x = 0;
-      if (b < P.B) {
-        const Request r = load_request<PATH>(P, b, false);
-        x = (long long)r.groups * HR * (r.tsa + r.tsw);
-      }
-      long long sum = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += a;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > begin);
-      if (hit != 0u) {
-        const int src = __ffs(hit) - 1;
-        cb = b0 + src;
-        const long long start = before + __shfl_sync(0xffffffffu, sum - x, src);
-        cr = load_request<PATH>(P, cb, false);
-        const int per_unit = cr.tsa + cr.tsw;
-        const long long rel = begin - start;
-        const long long uh = rel / per_unit;
-        ctile = int(rel - uh * per_unit);
-        cgrp = int(uh / HR);
-        chr_ = int(uh - (long long)cgrp * HR);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
+    const Place p = locate<PATH>(P, head, HR, begin);
+    cb = p.b;
+    cr = p.r;
+    const int per_unit = cr.tsa + cr.tsw;
+    const long long uh = p.off / per_unit;
+    ctile = int(p.off - uh * per_unit);
+    cgrp = int(uh / HR);
+    chr_ = int(uh - (long long)cgrp * HR);
   }
   bool done = false;
   auto next_unit = [&]() {  // to the first tile of the next unit, if any
@@ -216,7 +281,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
       cr = load_request<PATH>(P, cb, false);
     } while (cr.groups == 0 || cr.tsa + cr.tsw == 0);
   };
-  if (P.snap && ctile != 0) {  // the unit cut here is the previous worker's
+  if (snap && ctile != 0) {  // the unit cut here is the previous worker's
     cpos += cr.tsa + cr.tsw - ctile;
     next_unit();
   }
@@ -226,6 +291,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     int flags, pos0, rows, t0, hr, b, tok;  // tok: this lane's key (lane & 15), -1: none
   };
   int upos0 = 0, urows = 0, ut0 = 0, slo = 0, shi = 0, wlo = 0, whi = 0;
+  int have_b = -1, have_grp = -1;
   bool fresh = true;  // the cursor's unit has not been entered yet
   auto make = [&]() -> Tile {
     Tile t;
@@ -233,7 +299,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     t.flags = kNone;
     t.pos0 = t.rows = t.t0 = t.hr = t.b = 0;
     const int per_unit = cr.tsa + cr.tsw;
-    if (done || (P.snap ? (ctile == 0 && cpos >= end) : cpos >= end)) return t;
+    if (done || (snap ? (ctile == 0 && cpos >= end) : cpos >= end)) return t;
     int flags = 0;
     if (fresh) {
       const int i0 = cgrp * P.tb, nt = min(P.tb, cr.n - i0);
@@ -244,7 +310,9 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
         wlo = max(0, upos0 - P.w + 1);
         whi = upos0 + nt;
       }
-      if (PATH != kPathSWA) {
+      if (PATH != kPathSWA && (have_b != cb || have_grp != cgrp)) {  // one token's heads share it
+        have_b = cb;
+        have_grp = cgrp;
         const int p = P.inv[(long long)cb * P.perm_stride + upos0];
         slo = shi = 0;
         if (unsigned(p) < unsigned(P.perm_len)) {
@@ -257,13 +325,13 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
       flags |= kNewQ;
     }
     const long long ustart = cpos - ctile;
-    const bool whole = P.snap || (ustart >= begin && ustart + per_unit <= end);
+    const bool whole = snap || (ustart >= begin && ustart + per_unit <= end);
     if (whole) flags |= kWhole;
     if (ustart >= begin) flags |= kTail;
     if (fresh && !whole && ustart >= begin && lane == 0) {
       Desc d;
       d.valid = 1;
-      d.c1 = int((ustart + per_unit - 1) / per);
+      d.first = first;
       d.t0 = ut0;
       d.hr = chr_;
       d.nrows = urows;
@@ -271,6 +339,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
       d.tsw = cr.tsw;
       d.add_swa = PATH == kPathGated && cr.tsw == 0;
       d.u0 = ustart;
+      d.origin = origin;
       d.per = per;
       P.desc[worker] = d;
     }
@@ -280,7 +349,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     if (is_swa) flags |= kIsSwa;
     if (PATH == kPathGated && cr.tsw == 0) flags |= kAddSwa;
     const bool path_end = ctile == (is_swa ? per_unit : cr.tsa) - 1;
-    if (path_end || (!P.snap && cpos == end - 1)) flags |= kLast;
+    if (path_end || (!snap && cpos == end - 1)) flags |= kLast;
     // this lane's key
     const int key = pt * kKeys + (lane & 15);
     if (is_swa) {
@@ -288,14 +357,8 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
       if (j < whi) t.tok = j;
     } else {
       const int j = slo + key;
-      if (j < shi) {
-        const int tok = P.perm[(long long)cb * P.perm_stride + j];
-        if (unsigned(tok) >= unsigned(P.perm_len)) {
-          atomicOr(P.err, SA_ERRBIT_RANGE);
-        } else if (tok <= upos0) {
-          t.tok = tok;
-        }
-      }
+      if (j < shi) t.tok = P.perm[(long long)cb * P.perm_stride + j];
+      flags |= j < shi ? kRaw : 0;
     }
     t.flags = flags;
     t.pos0 = upos0;
@@ -310,6 +373,17 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
       fresh = true;
     }
     return t;
+  };
+  // sigma's entries are looked at a step after their loads began
+  auto settle = [&](Tile& t) {
+    if (PATH == kPathSWA || !(t.flags & kRaw)) return;
+    t.flags &= ~kRaw;
+    if (unsigned(t.tok) >= unsigned(P.perm_len)) {
+      atomicOr(P.err, SA_ERRBIT_RANGE);
+      t.tok = -1;
+    } else if (t.tok > t.pos0) {
+      t.tok = -1;  // a later token
+    }
   };
   auto page_of = [&](const Tile& t) {  // -1: no key
     return t.tok >= 0 ? P.table[(long long)t.b * P.max_pages + int(unsigned(t.tok) / unsigned(P.page))] : -1;
@@ -366,12 +440,14 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
 
   // ---- the pipeline
   Tile ta = make();
+  settle(ta);
   int pa = page_of(ta);
   Tile tn = make();
   auto step = [&](int stage) {
     issue(ta, pa, stage);
     asm volatile("cp.async.commit_group;" ::: "memory");
     ta = tn;
+    settle(ta);
     pa = page_of(ta);
     tn = make();
   };
@@ -579,17 +655,14 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Joins the partials of each unit that the runs cut: block c takes the unit
-// that starts in worker c's run.  Piece after piece in worker order.
+// Joins the parts of the unit that starts in worker c0's run, piece after
+// piece in worker order.
 template <int D, int PATH>
-__global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constant__ Params P) {
-  const Desc d = P.desc[blockIdx.x];
-  if (!d.valid) return;
-  const int c0 = blockIdx.x;
+__device__ __forceinline__ void join_unit(const Params& P, const Desc& d, int c0, int tid, int threads) {
   const int kvh = d.hr / P.rg;
   const int h0 = kvh * P.g + (P.rg > 1 ? (d.hr - kvh * P.rg) * 16 : 0);
   constexpr int kPaths = PATH == kPathGated ? 2 : 1;
-  for (int i = threadIdx.x; i < d.nrows * (D / 4); i += 128) {
+  for (int i = tid; i < d.nrows * (D / 4); i += threads) {
     const int r = i / (D / 4), c4 = i - r * (D / 4);
     const int tk = P.rg > 1 ? 0 : r / P.g;
     const size_t row = size_t(d.t0 + tk) * P.Hq + h0 + r - tk * P.g;
@@ -599,14 +672,16 @@ __global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constan
       const bool is_swa = PATH == kPathSWA || path == 1;
       const long long lo = d.u0 + (is_swa ? d.tsa : 0), hi = lo + (is_swa ? d.tsw : d.tsa);
       if (hi <= lo) continue;
-      const int ca = int(lo / d.per), cz = int((hi - 1) / d.per);
+      const int ca = d.first + int((lo - d.origin) / d.per), cz = d.first + int((hi - 1 - d.origin) / d.per);
       auto piece = [&](int c) {
         return P.part + (size_t(c * 2 + (c == c0 ? 1 : 0)) * kPaths + path) * P.slot_floats;
       };
       float m = -INFINITY;
+#pragma unroll 4
       for (int c = ca; c <= cz; ++c) m = fmaxf(m, piece(c)[P.R * D + 2 * r]);
       float l = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int c = ca; c <= cz; ++c) {
         const float* pw = piece(c);
         const float pm = pw[P.R * D + 2 * r];
@@ -636,10 +711,33 @@ __global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constan
   }
 }
 
+template <int D, int PATH>
+__global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(const __grid_constant__ Params P) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  // the join kernel may be put on SMs that this grid has left
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  run_worker<D, PATH>(P, smem_raw);
+  if (P.mode == kBlocks) {
+    __syncthreads();  // every warp's parts are written
+    for (int w = 0; w < P.warps; ++w) {
+      const int c = int(blockIdx.x) * P.warps + w;
+      const Desc d = P.desc[c];
+      if (d.valid) join_unit<D, PATH>(P, d, c, threadIdx.x, blockDim.x);
+    }
+  }
+}
+
+template <int D, int PATH>
+__global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's writes
+  const Desc d = P.desc[blockIdx.x];
+  if (d.valid) join_unit<D, PATH>(P, d, blockIdx.x, threadIdx.x, 128);
+}
+
 // ------------------------------------------------------------------ host
 
 struct Config {
-  int tb, rg, R, slot_floats, warps, workers, split, min_tiles;
+  int tb, rg, R, slot_floats, warps, workers, mode, min_tiles;
   uint32_t stage_bytes, warp_bytes;
   size_t part_bytes, desc_bytes;
 };
@@ -659,30 +757,38 @@ static Config make_config(const PagedProblem& pb, Path path, int row_limit, int 
   const int most_warps = pb.d == 128 ? 8 : 16;
   if (c.warps > most_warps) c.warps = most_warps;
   c.workers = sms * c.warps;
-  // Runs end at unit ends, without partials, where there are at least four
-  // units per worker of at most 1024 keys each.
+  // Units short enough to leave whole to a worker (at least four of them for
+  // each) or to a block; longer ones are cut over the GPU.
   const long long units = (pb.T + c.tb - 1) / c.tb * (long long)pb.Hkv * c.rg;
-  const long long keys = path == kPathSA ? 2LL * pb.half + 1
-                         : path == kPathSWA ? (long long)pb.window_swa
-                                            : 2LL * pb.half + 1 + pb.window_swa;
-  c.split = !(units >= 4LL * c.workers && keys <= 1024);
-  c.min_tiles = 4;
-  c.part_bytes = c.split ? (size_t(c.workers) * 2 * (path == kPathGated ? 2 : 1) * c.slot_floats * 4 + 255) / 256 * 256
-                         : 0;
-  c.desc_bytes = c.split ? size_t(c.workers) * sizeof(Desc) : 0;
+  const long long longest = min((long long)pb.window_swa + c.tb - 1, (long long)pb.max_pages * pb.page);
+  const long long around = min(2LL * pb.half + 1, (long long)pb.perm_len);
+  const long long keys = path == kPathSA ? around : path == kPathSWA ? longest : around + longest;
+  c.mode = keys > 1280 ? kCut : units >= 4LL * c.workers ? kWarps : kBlocks;
+  c.min_tiles = c.mode == kCut ? 4 : 1;
+  c.part_bytes = c.mode == kWarps ? 0
+                                  : (size_t(c.workers) * 2 * (path == kPathGated ? 2 : 1) * c.slot_floats * 4 + 255) / 256 * 256;
+  c.desc_bytes = c.mode == kWarps ? 0 : size_t(c.workers) * sizeof(Desc);
   return c;
 }
 
 template <int D, int PATH>
 static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStream_t stream) {
   const uint32_t smem = c.warp_bytes * uint32_t(c.warps);
-  cudaError_t ce = cudaFuncSetAttribute(sa_paged_rows_kernel<D, PATH>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
+  cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH>>(kMaxSmem);
   if (ce != cudaSuccess) return ce;
   sa_paged_rows_kernel<D, PATH><<<sms, 32 * c.warps, smem, stream>>>(P);
-  if ((ce = cudaGetLastError()) != cudaSuccess || !c.split) return ce;
-  sa_paged_join_kernel<D, PATH><<<c.workers, 128, 0, stream>>>(P);
-  return cudaGetLastError();
+  if ((ce = cudaGetLastError()) != cudaSuccess || c.mode != kCut) return ce;
+  // its blocks may be set up while the row kernel's last ones finish
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(c.workers));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sa_paged_join_kernel<D, PATH>, P);
 }
 
 }  // namespace prow
@@ -711,7 +817,7 @@ sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
   P.swa_part = swa_part;
   P.out = static_cast<__nv_bfloat16*>(pb.out);
   P.err = pb.err;
-  if (c.split) {
+  if (c.mode != kWarps) {
     P.part = static_cast<float*>(part);
     P.desc = reinterpret_cast<Desc*>(static_cast<char*>(part) + c.part_bytes);
   }
@@ -737,7 +843,8 @@ sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
   P.slot_floats = c.slot_floats;
   P.workers = c.workers;
   P.min_tiles = c.min_tiles;
-  P.snap = c.split ? 0 : 1;
+  P.mode = c.mode;
+  P.warps = c.warps;
   P.stage_bytes = c.stage_bytes;
   P.warp_bytes = c.warp_bytes;
   P.scale_log2 = pb.scale * 1.4426950408889634f;

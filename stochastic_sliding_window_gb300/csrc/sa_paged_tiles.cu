@@ -968,8 +968,7 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
   const uint32_t smem = P.off_bar + 8 * Bars<NS>::kNum + 16 + 1024;
   static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(Keys) + 4 * sizeof(Shared) + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
                     kMaxSmem, "shared memory");
-  cudaError_t ce = cudaFuncSetAttribute(sa_paged_tiles_kernel<D, NS>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS>>(smem);
   if (ce != cudaSuccess) return ce;
   sa_paged_tiles_kernel<D, NS><<<sms, kThreads, smem, stream>>>(P);
   if ((ce = cudaGetLastError()) != cudaSuccess || P.desc == nullptr) return ce;
