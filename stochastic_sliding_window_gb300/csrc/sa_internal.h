@@ -173,6 +173,15 @@ struct PagedProblem {
 size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int row_limit, int sms);
 sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
                               const float* swa_part, void* part, int sms, cudaStream_t stream);
+// A unit of it: tokens, row groups of a kv head, rows; and its most keys.
+void paged_unit_shape(const PagedProblem& pb, Path path, int row_limit, int* tb, int* rg, int* rows);
+long long paged_unit_keys(const PagedProblem& pb, Path path, int tb);
+
+// Unit kernel (sa_paged_unit.cu): the same for few units of few keys, a block
+// each; no workspace.
+bool paged_unit_fits(const PagedProblem& pb, Path path, int row_limit, int sms);
+sa_status_t launch_paged_unit(const PagedProblem& pb, Path path, int row_limit,
+                              const float* swa_part, cudaStream_t stream);
 
 // Tile kernel (sa_paged_tiles.cu): the SWA path of requests with more than
 // row_limit new tokens, into pb.out; with `gate` (logits [T, Hq]) as fp32

@@ -1,7 +1,8 @@
 // Serving over a paged K/V cache: the C-ABI entry points, the plan of a step
 // (block tables, slots and positions from the requests' lengths) and the
 // writer of new keys and values.  The attention itself is in
-// sa_paged_rows.cu (few new tokens) and sa_paged_tiles.cu (many).
+// sa_paged_rows.cu and sa_paged_unit.cu (few new tokens) and sa_paged_tiles.cu
+// (many).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -407,16 +408,22 @@ static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
 constexpr int kRowLimit = 64;
 
 struct Choice {
-  bool tiles, rows;
+  bool tiles, rows, unit;
   int row_limit;  // new tokens per request that the row kernel still takes
 };
 
-static Choice choose(const PagedProblem& pb, Path path, int kernel) {
-  Choice c{false, true, 0x7fffffff};
-  if (path == kPathSA || kernel == SA_PAGED_ROWS || !paged_tiles_supported(pb)) return c;
-  if (kernel == SA_PAGED_TILES) return Choice{true, false, 0};
-  const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
-  if (pb.max_new > limit) c = Choice{true, true, limit};
+static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
+  Choice c{false, true, false, 0x7fffffff};
+  if (path != kPathSA && kernel != SA_PAGED_ROWS && paged_tiles_supported(pb)) {
+    if (kernel == SA_PAGED_TILES) return Choice{true, false, false, 0};
+    const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
+    if (pb.max_new > limit) c = Choice{true, true, false, limit};
+  }
+  // few units of few keys: the unit kernel instead of the row kernel
+  if (paged_unit_fits(pb, path, c.row_limit, sms)) {
+    c.unit = true;
+    c.rows = false;
+  }
   return c;
 }
 
@@ -456,7 +463,7 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   const int sms = dev.sms;
   if (sms == 0) return fail(SA_ERR_UNSUPPORTED, "device is not sm_103");
   PagedProblem pb = make_problem(prm, path);
-  const Choice ch = choose(pb, path, prm->kernel);
+  const Choice ch = choose(pb, path, prm->kernel, sms);
   if (prm->kernel == SA_PAGED_TILES && !ch.tiles)
     return fail(SA_ERR_UNSUPPORTED, "the tile kernel takes at most 64 query heads per kv head");
   const Workspace parts = workspace_parts(pb, path, ch, sms);
@@ -478,6 +485,10 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   float* const swa_part = parts.swa_part ? reinterpret_cast<float*>(w + parts.rows + parts.tiles) : nullptr;
   if (ch.tiles) {
     st = launch_paged_tiles(pb, ch.row_limit, gate_swa, swa_part, w + parts.rows, sms, stream);
+    if (st != SA_OK) return st;
+  }
+  if (ch.unit) {
+    st = launch_paged_unit(pb, path, ch.row_limit, swa_part, stream);
     if (st != SA_OK) return st;
   }
   if (ch.rows) {
@@ -526,7 +537,7 @@ extern "C" size_t sa_paged_workspace_size(const sa_paged_params_t* params, int32
   if (!device_info(&dev) || dev.sms == 0) return 0;
   const int sms = dev.sms;
   const PagedProblem pb = paged::make_problem(params, pt);
-  return paged::workspace_parts(pb, pt, paged::choose(pb, pt, params->kernel), sms).total();
+  return paged::workspace_parts(pb, pt, paged::choose(pb, pt, params->kernel, sms), sms).total();
 }
 
 extern "C" sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cached_lens,

@@ -19,24 +19,18 @@
 // whatever the lengths are and the host needs to know none.  A warp works
 // alone -- its own ring of cp.async stages, no block barriers -- and its
 // loads run ahead across the ends of units.  A unit cut by a run's end leaves
-// fp32 partials (O, m, l) in the workspace, which are joined in worker order,
-// so results do not depend on timing: by the second kernel where runs are cut
-// over the whole GPU (long keys), by the block itself where a unit stays in
-// one block (windows of up to about a thousand keys); with several such units
-// per worker a unit is left to one warp and there is nothing to join.
-#include "sa_internal.h"
-#include "sa_tc_common.cuh"
+// fp32 partials (O, m, l) in the workspace, which the second kernel joins in
+// worker order, so results do not depend on timing.  Where there are several
+// short units per worker the runs end at unit ends and there is nothing to
+// join.  (Few short units: sa_paged_unit.cu.)
+#include "sa_paged_rows.cuh"
 
 #include <cstring>
 
 namespace sa {
 namespace prow {
 
-using namespace tcc;
-
-constexpr int kKeys = 16;   // keys per tile
 constexpr int kStages = 3;
-constexpr uint32_t kMaxSmem = 232448;
 constexpr int kMetaInts = 32;  // 16 key tokens, then the fields below
 enum : int { kFlags = 16, kPos0, kRows, kTok0, kHr };
 enum : int {
@@ -51,94 +45,6 @@ enum : int {
   kNone = 256,    // no tile: the run is done
   kRaw = 512,     // (this lane) the key is an entry of sigma not yet looked at
 };
-
-struct Desc {  // one per worker: the unit that starts in its run and ends beyond it
-  int valid, t0, hr, nrows, tsa, tsw, add_swa, first;
-  long long u0, origin, per;  // tile x lies in the run of worker first + (x - origin) / per
-};
-
-// How the tiles are cut into runs.
-enum : int {
-  kCut = 0,     // equal runs, cut anywhere; the join kernel merges the parts
-  kWarps = 1,   // a unit belongs to the run it starts in: nothing to merge
-  kBlocks = 2,  // a unit belongs to the block whose run it starts in; the
-                // block's warps cut their share anywhere and merge it themselves
-};
-
-struct Params {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  const int32_t* table;
-  const int32_t* q_start;
-  const int32_t* seq_lens;
-  const int32_t* perm;
-  const int32_t* inv;
-  const float* gate_sa;
-  const float* gate_swa;
-  const float* swa_part;  // [T, Hq, D] gated SWA terms of requests beyond row_limit
-  __nv_bfloat16* out;
-  int32_t* err;
-  float* part;            // partial slots, then Desc[workers]; nullptr: never split
-  Desc* desc;
-  long long q_stride, page_stride, perm_stride;
-  int B, T, max_new, row_limit, Hq, Hkv, g, page, num_pages, max_pages;
-  int w, half, perm_len;
-  int tb, rg, R;          // tokens and rows of a unit; row groups of a kv head (g > 16)
-  int slot_floats;        // one partial: O [R, D], then (m, l) [R]; a multiple of 4
-  int warps, workers, min_tiles, mode;
-  uint32_t stage_bytes, warp_bytes;
-  float scale_log2;
-};
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-               "{%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// A request as the units see it; n = 0 where it has none here.
-struct Request {
-  int q0, n, len, tsa, tsw, groups;
-};
-
-template <int PATH>
-__device__ __forceinline__ Request load_request(const Params& P, int b, bool report) {
-  Request r;
-  r.q0 = P.q_start[b];
-  const int q1 = P.q_start[b + 1];
-  r.len = P.seq_lens[b];
-  r.n = q1 - r.q0;
-  r.tsa = r.tsw = 0;
-  const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= P.T && r.n <= P.max_new && r.n <= r.len &&
-                  (long long)r.len <= (long long)P.max_pages * P.page &&
-                  (PATH == kPathSWA || r.len <= P.perm_len);
-  if (!ok) {
-    // (a request without new tokens is not looked at otherwise)
-    if (report && q1 != r.q0) atomicOr(P.err, SA_ERRBIT_RANGE);
-    r.n = 0;
-  }
-  const bool swa_here = r.n <= P.row_limit;
-  if (PATH == kPathSWA && !swa_here) r.n = 0;
-  if (PATH != kPathSWA) r.tsa = int((min(2LL * P.half + 1, (long long)P.perm_len) + kKeys - 1) / kKeys);
-  if (PATH != kPathSA && swa_here)
-    r.tsw = int((min((long long)r.len, (long long)P.w + P.tb - 1) + kKeys - 1) / kKeys);
-  r.groups = ceil_div(r.n, P.tb);
-  return r;
-}
 
 // Where a position of the laid-out tiles lies: request, its fields, and the
 // position's offset in the request's tiles.  All lanes of a warp call it.
@@ -197,27 +103,17 @@ __device__ __forceinline__ Place locate(const Params& P, const Scan& head, int H
   }
 }
 
-// The first unit start at or after pos.
-template <int PATH>
-__device__ __forceinline__ long long unit_from(const Params& P, const Scan& head, int HR, long long pos,
-                                               long long total) {
-  if (pos >= total) return total;
-  const Place p = locate<PATH>(P, head, HR, pos);
-  const int per_unit = p.r.tsa + p.r.tsw;
-  const int in = int(p.off % per_unit);
-  return in == 0 ? pos : pos + per_unit - in;
-}
-
-// One warp's run of tiles.
 template <int D, int PATH>
-__device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
-  constexpr int kPitch = D * 2 + 16;  // 16 bytes over: eight rows of a matrix hit all banks
-  constexpr int kCpr = D / 8;         // 16-byte chunks per row
+__global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(const __grid_constant__ Params P) {
+  constexpr int kPitch = Pitch<D>;
+  constexpr int kCpr = D / 8;  // 16-byte chunks per row
   constexpr uint32_t kOffV = kKeys * kPitch, kOffQ = 2 * kKeys * kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // runs that follow each other on different SMs, or in one block
-  const int worker = P.mode == kBlocks ? int(blockIdx.x) * P.warps + warp : warp * int(gridDim.x) + int(blockIdx.x);
-  uint8_t* ring = smem + size_t(warp) * P.warp_bytes;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  // the join kernel's blocks may be put on SMs that this grid has left
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int worker = warp * int(gridDim.x) + int(blockIdx.x);
+  uint8_t* ring = smem_raw + size_t(warp) * P.warp_bytes;
   const uint32_t sring = smem_u32(ring);
   const uint32_t off_meta = kOffQ + uint32_t(P.R) * kPitch;
   const int HR = P.Hkv * P.rg;
@@ -235,22 +131,12 @@ __device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
     for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
     total += more;
   }
-  long long origin = 0, limit = total, per;
-  int first = 0;
-  if (P.mode == kBlocks) {
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
-    first = int(blockIdx.x) * P.warps;
-    origin = unit_from<PATH>(P, head, HR, share * blockIdx.x, total);
-    limit = unit_from<PATH>(P, head, HR, share * (blockIdx.x + 1), total);
-    per = max((limit - origin + P.warps - 1) / P.warps, (long long)P.min_tiles);
-  } else {
-    per = max((total + P.workers - 1) / P.workers, (long long)P.min_tiles);
-  }
-  const bool snap = P.mode == kWarps;
-  const long long begin = origin + per * (worker - first);
-  const long long end = min(limit, begin + per);
+  const long long per = max((total + P.workers - 1) / P.workers, (long long)P.min_tiles);
+  const long long begin = per * worker;
+  const long long end = min(total, begin + per);
+  const bool snap = P.snap != 0;
   if (P.desc != nullptr && lane == 0) P.desc[worker].valid = 0;
-  if (begin >= limit) return;
+  if (begin >= total) return;
 
   // ---- cursor: request, group, head and tile of the next tile to fetch
   int cb, cgrp, chr_, ctile;
@@ -331,15 +217,14 @@ __device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
     if (fresh && !whole && ustart >= begin && lane == 0) {
       Desc d;
       d.valid = 1;
-      d.first = first;
       d.t0 = ut0;
       d.hr = chr_;
       d.nrows = urows;
       d.tsa = cr.tsa;
       d.tsw = cr.tsw;
       d.add_swa = PATH == kPathGated && cr.tsw == 0;
+      d.pad = 0;
       d.u0 = ustart;
-      d.origin = origin;
       d.per = per;
       P.desc[worker] = d;
     }
@@ -455,9 +340,11 @@ __device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
   step(1);
 
   uint32_t qf[D / 16][4];
-  float o[D / 8][4];
+  Acc<D> acc;
+  float (&o)[D / 8][4] = acc.o;
+  float &m0 = acc.m0, &m1 = acc.m1, &l0 = acc.l0, &l1 = acc.l1;
   float stash[PATH == kPathGated ? D / 8 : 1][4];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  acc.reset();
   const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows of the unit
   const int rt0 = P.rg > 1 ? 0 : r0 / P.g, rt1 = P.rg > 1 ? 0 : r1 / P.g;
   int stage = 0, fill = kStages - 1;
@@ -473,121 +360,25 @@ __device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
     if (flags & kNone) break;
     const int pos0 = meta[kPos0], rows = meta[kRows];
     if (flags & kFirst) {
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      acc.reset();
     }
     if (flags & kNewQ) {
-      // rows past the unit's last read its first: their weights are all masked
-      int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-      if (r >= rows) r = 0;
-      const uint32_t a = ss + kOffQ + r * kPitch + (lane >> 4) * 16;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) ldsm4(a + i * 32, qf[i]);
+      load_q<D>(ss + kOffQ, rows, qf);
     }
     if (flags & kAny) {
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const uint32_t a = ss + ((lane & 7) + (lane >> 4) * 8) * kPitch + ((lane >> 3) & 1) * 16;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t kf[4];
-          ldsm4(a + i * 32, kf);
-          mma16816(s[0], qf[i], kf[0], kf[1]);
-          mma16816(s[1], qf[i], kf[2], kf[3]);
-        }
-      }
       const unsigned w = PATH == kPathSWA || (flags & kIsSwa) ? unsigned(P.w) : 0x7fffffffu;
       const int p0 = r0 < rows ? pos0 + rt0 : -1, p1 = r1 < rows ? pos0 + rt1 : -1;
-      float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int2 tok = *reinterpret_cast<const int2*>(meta + t * 8 + (lane & 3) * 2);
-        s[t][0] = unsigned(p0 - tok.x) < w ? s[t][0] * P.scale_log2 : -INFINITY;
-        s[t][1] = unsigned(p0 - tok.y) < w ? s[t][1] * P.scale_log2 : -INFINITY;
-        s[t][2] = unsigned(p1 - tok.x) < w ? s[t][2] * P.scale_log2 : -INFINITY;
-        s[t][3] = unsigned(p1 - tok.y) < w ? s[t][3] * P.scale_log2 : -INFINITY;
-        x0 = fmax3(x0, s[t][0], s[t][1]);
-        x1 = fmax3(x1, s[t][2], s[t][3]);
-      }
-#pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-      }
-      if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
-        const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a0;
-          o[i][2] *= a1;
-          o[i][3] *= a1;
-        }
-      }
-      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float e0 = fast_exp2(s[t][0] - b0), e1 = fast_exp2(s[t][1] - b0);
-        const float e2 = fast_exp2(s[t][2] - b1), e3 = fast_exp2(s[t][3] - b1);
-        l0 += e0 + e1;
-        l1 += e2 + e3;
-        hi[2 * t] = pack_bf16x2(e0, e1);
-        hi[2 * t + 1] = pack_bf16x2(e2, e3);
-        lo[2 * t] = pack_bf16x2(e0 - __uint_as_float(hi[2 * t] << 16), e1 - __uint_as_float(hi[2 * t] & 0xffff0000u));
-        lo[2 * t + 1] = pack_bf16x2(e2 - __uint_as_float(hi[2 * t + 1] << 16),
-                                    e3 - __uint_as_float(hi[2 * t + 1] & 0xffff0000u));
-      }
-      const uint32_t a = ss + kOffV + ((lane & 7) + ((lane >> 3) & 1) * 8) * kPitch + (lane >> 4) * 16;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t vf[4];
-        ldsm4t(a + i * 32, vf);
-        mma16816(o[2 * i], hi, vf[0], vf[1]);
-        mma16816(o[2 * i + 1], hi, vf[2], vf[3]);
-        mma16816(o[2 * i], lo, vf[0], vf[1]);
-        mma16816(o[2 * i + 1], lo, vf[2], vf[3]);
-      }
+      acc.tile(ss, ss + kOffV, meta, qf, p0, p1, w, P.scale_log2);
     }
     if (flags & kLast) {
       const int t0 = meta[kTok0], hr = meta[kHr];
       const int kvh = hr / P.rg;
       const int h0 = kvh * P.g + (P.rg > 1 ? (hr - kvh * P.rg) * 16 : 0);
-#pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-      }
+      acc.sum_rows();
       if (!(flags & kWhole)) {
         const int slot = (worker * 2 + ((flags & kTail) ? 1 : 0)) * (PATH == kPathGated ? 2 : 1) +
                          (PATH == kPathGated && (flags & kIsSwa) ? 1 : 0);
-        float* pw = P.part + size_t(slot) * P.slot_floats;
-        if (r0 < rows) {
-          if ((lane & 3) == 0) {
-            pw[P.R * D + 2 * r0] = m0;
-            pw[P.R * D + 2 * r0 + 1] = l0;
-          }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(pw + r0 * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][0], o[i][1]);
-        }
-        if (r1 < rows) {
-          if ((lane & 3) == 0) {
-            pw[P.R * D + 2 * r1] = m1;
-            pw[P.R * D + 2 * r1 + 1] = l1;
-          }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(pw + r1 * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][2], o[i][3]);
-        }
+        acc.write(P.part + size_t(slot) * P.slot_floats, P.R, rows);
       } else {
         float f0 = l0 == 0.f ? 0.f : 1.f / l0, f1 = l1 == 0.f ? 0.f : 1.f / l1;
         const size_t row0 = size_t(t0 + rt0) * P.Hq + h0 + r0 - rt0 * P.g;
@@ -655,14 +446,18 @@ __device__ __forceinline__ void run_worker(const Params& P, uint8_t* smem) {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Joins the parts of the unit that starts in worker c0's run, piece after
-// piece in worker order.
+// Joins the parts of each unit that the runs cut, piece after piece in worker
+// order: block c takes the unit that starts in worker c's run.
 template <int D, int PATH>
-__device__ __forceinline__ void join_unit(const Params& P, const Desc& d, int c0, int tid, int threads) {
+__global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's writes
+  const Desc d = P.desc[blockIdx.x];
+  if (!d.valid) return;
+  const int c0 = blockIdx.x;
   const int kvh = d.hr / P.rg;
   const int h0 = kvh * P.g + (P.rg > 1 ? (d.hr - kvh * P.rg) * 16 : 0);
   constexpr int kPaths = PATH == kPathGated ? 2 : 1;
-  for (int i = tid; i < d.nrows * (D / 4); i += threads) {
+  for (int i = threadIdx.x; i < d.nrows * (D / 4); i += 128) {
     const int r = i / (D / 4), c4 = i - r * (D / 4);
     const int tk = P.rg > 1 ? 0 : r / P.g;
     const size_t row = size_t(d.t0 + tk) * P.Hq + h0 + r - tk * P.g;
@@ -672,7 +467,7 @@ __device__ __forceinline__ void join_unit(const Params& P, const Desc& d, int c0
       const bool is_swa = PATH == kPathSWA || path == 1;
       const long long lo = d.u0 + (is_swa ? d.tsa : 0), hi = lo + (is_swa ? d.tsw : d.tsa);
       if (hi <= lo) continue;
-      const int ca = d.first + int((lo - d.origin) / d.per), cz = d.first + int((hi - 1 - d.origin) / d.per);
+      const int ca = int(lo / d.per), cz = int((hi - 1) / d.per);
       auto piece = [&](int c) {
         return P.part + (size_t(c * 2 + (c == c0 ? 1 : 0)) * kPaths + path) * P.slot_floats;
       };
@@ -711,44 +506,17 @@ __device__ __forceinline__ void join_unit(const Params& P, const Desc& d, int c0
   }
 }
 
-template <int D, int PATH>
-__global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(const __grid_constant__ Params P) {
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  // the join kernel may be put on SMs that this grid has left
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  run_worker<D, PATH>(P, smem_raw);
-  if (P.mode == kBlocks) {
-    __syncthreads();  // every warp's parts are written
-    for (int w = 0; w < P.warps; ++w) {
-      const int c = int(blockIdx.x) * P.warps + w;
-      const Desc d = P.desc[c];
-      if (d.valid) join_unit<D, PATH>(P, d, c, threadIdx.x, blockDim.x);
-    }
-  }
-}
-
-template <int D, int PATH>
-__global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constant__ Params P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's writes
-  const Desc d = P.desc[blockIdx.x];
-  if (d.valid) join_unit<D, PATH>(P, d, blockIdx.x, threadIdx.x, 128);
-}
-
 // ------------------------------------------------------------------ host
 
 struct Config {
-  int tb, rg, R, slot_floats, warps, workers, mode, min_tiles;
+  int tb, rg, R, slot_floats, warps, workers, snap;
   uint32_t stage_bytes, warp_bytes;
   size_t part_bytes, desc_bytes;
 };
 
 static Config make_config(const PagedProblem& pb, Path path, int row_limit, int sms) {
   Config c;
-  c.rg = (pb.g + 15) / 16;
-  // several tokens share a unit's 16 rows only where they share a window
-  const int most_new = min(pb.max_new, row_limit);
-  c.tb = path == kPathSWA && pb.g < 16 ? min(16 / pb.g, most_new) : 1;
-  c.R = c.rg > 1 ? 16 : c.tb * pb.g;
+  paged_unit_shape(pb, path, row_limit, &c.tb, &c.rg, &c.R);
   c.slot_floats = (c.R * (pb.d + 2) + 3) / 4 * 4;  // 16-byte aligned slots
   const uint32_t pitch = uint32_t(pb.d) * 2 + 16;
   c.stage_bytes = (2 * kKeys + uint32_t(c.R)) * pitch + kMetaInts * 4;
@@ -757,17 +525,12 @@ static Config make_config(const PagedProblem& pb, Path path, int row_limit, int 
   const int most_warps = pb.d == 128 ? 8 : 16;
   if (c.warps > most_warps) c.warps = most_warps;
   c.workers = sms * c.warps;
-  // Units short enough to leave whole to a worker (at least four of them for
-  // each) or to a block; longer ones are cut over the GPU.
+  // Short units are left whole where there are at least four for each worker.
   const long long units = (pb.T + c.tb - 1) / c.tb * (long long)pb.Hkv * c.rg;
-  const long long longest = min((long long)pb.window_swa + c.tb - 1, (long long)pb.max_pages * pb.page);
-  const long long around = min(2LL * pb.half + 1, (long long)pb.perm_len);
-  const long long keys = path == kPathSA ? around : path == kPathSWA ? longest : around + longest;
-  c.mode = keys > 1280 ? kCut : units >= 4LL * c.workers ? kWarps : kBlocks;
-  c.min_tiles = c.mode == kCut ? 4 : 1;
-  c.part_bytes = c.mode == kWarps ? 0
-                                  : (size_t(c.workers) * 2 * (path == kPathGated ? 2 : 1) * c.slot_floats * 4 + 255) / 256 * 256;
-  c.desc_bytes = c.mode == kWarps ? 0 : size_t(c.workers) * sizeof(Desc);
+  c.snap = units >= 4LL * c.workers && paged_unit_keys(pb, path, c.tb) <= 1280;
+  c.part_bytes =
+      c.snap ? 0 : (size_t(c.workers) * 2 * (path == kPathGated ? 2 : 1) * c.slot_floats * 4 + 255) / 256 * 256;
+  c.desc_bytes = c.snap ? 0 : size_t(c.workers) * sizeof(Desc);
   return c;
 }
 
@@ -777,7 +540,7 @@ static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStr
   cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH>>(kMaxSmem);
   if (ce != cudaSuccess) return ce;
   sa_paged_rows_kernel<D, PATH><<<sms, 32 * c.warps, smem, stream>>>(P);
-  if ((ce = cudaGetLastError()) != cudaSuccess || c.mode != kCut) return ce;
+  if ((ce = cudaGetLastError()) != cudaSuccess || c.snap) return ce;
   // its blocks may be set up while the row kernel's last ones finish
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(c.workers));
@@ -791,17 +554,7 @@ static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStr
   return cudaLaunchKernelEx(&cfg, sa_paged_join_kernel<D, PATH>, P);
 }
 
-}  // namespace prow
-
-size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int row_limit, int sms) {
-  const prow::Config c = prow::make_config(pb, path, row_limit, sms);
-  return c.part_bytes + c.desc_bytes;
-}
-
-sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
-                              const float* swa_part, void* part, int sms, cudaStream_t stream) {
-  using namespace prow;
-  const Config c = make_config(pb, path, row_limit, sms);
+void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, const float* swa_part) {
   Params P;
   std::memset(&P, 0, sizeof(P));
   P.q = static_cast<const __nv_bfloat16*>(pb.q);
@@ -817,10 +570,6 @@ sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
   P.swa_part = swa_part;
   P.out = static_cast<__nv_bfloat16*>(pb.out);
   P.err = pb.err;
-  if (c.mode != kWarps) {
-    P.part = static_cast<float*>(part);
-    P.desc = reinterpret_cast<Desc*>(static_cast<char*>(part) + c.part_bytes);
-  }
   P.q_stride = pb.q_stride;
   P.page_stride = pb.page_stride;
   P.perm_stride = pb.perm_rows == 1 ? 0 : pb.perm_len;
@@ -837,17 +586,48 @@ sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
   P.w = pb.window_swa;
   P.half = pb.half;
   P.perm_len = pb.perm_len;
-  P.tb = c.tb;
-  P.rg = c.rg;
-  P.R = c.R;
+  paged_unit_shape(pb, path, row_limit, &P.tb, &P.rg, &P.R);
+  P.scale_log2 = pb.scale * 1.4426950408889634f;
+  *out = P;
+}
+
+}  // namespace prow
+
+// Units: several tokens share the 16 rows only where they share a window.
+void paged_unit_shape(const PagedProblem& pb, Path path, int row_limit, int* tb, int* rg, int* rows) {
+  *rg = (pb.g + 15) / 16;
+  *tb = path == kPathSWA && pb.g < 16 ? min(16 / pb.g, min(pb.max_new, row_limit)) : 1;
+  *rows = *rg > 1 ? 16 : *tb * pb.g;
+}
+
+// The most keys that a unit attends to.
+long long paged_unit_keys(const PagedProblem& pb, Path path, int tb) {
+  const long long swa = min((long long)pb.window_swa + tb - 1, (long long)pb.max_pages * pb.page);
+  const long long near = min(2LL * pb.half + 1, (long long)pb.perm_len);
+  return path == kPathSWA ? swa : path == kPathSA ? near : swa + near;
+}
+
+size_t paged_rows_workspace_bytes(const PagedProblem& pb, Path path, int row_limit, int sms) {
+  const prow::Config c = prow::make_config(pb, path, row_limit, sms);
+  return c.part_bytes + c.desc_bytes;
+}
+
+sa_status_t launch_paged_rows(const PagedProblem& pb, Path path, int row_limit,
+                              const float* swa_part, void* part, int sms, cudaStream_t stream) {
+  using namespace prow;
+  const Config c = make_config(pb, path, row_limit, sms);
+  Params P;
+  fill_params(&P, pb, path, row_limit, swa_part);
+  if (!c.snap) {
+    P.part = static_cast<float*>(part);
+    P.desc = reinterpret_cast<Desc*>(static_cast<char*>(part) + c.part_bytes);
+  }
   P.slot_floats = c.slot_floats;
   P.workers = c.workers;
-  P.min_tiles = c.min_tiles;
-  P.mode = c.mode;
-  P.warps = c.warps;
+  P.min_tiles = 4;
+  P.snap = c.snap;
   P.stage_bytes = c.stage_bytes;
   P.warp_bytes = c.warp_bytes;
-  P.scale_log2 = pb.scale * 1.4426950408889634f;
   cudaError_t ce;
   if (pb.d == 128)
     ce = path == kPathSWA ? launch_one<128, kPathSWA>(P, c, sms, stream)
