@@ -353,7 +353,7 @@ typedef struct sa_paged_params {
   float softmax_scale;   /* <= 0 means 1/sqrt(head_dim) */
   int32_t reserved;      /* 0 */
   int64_t q_stride;      /* elements between tokens of q; 0: num_q_heads * head_dim; a multiple of 8 */
-  int64_t page_stride;   /* elements between pages of either cache; 0: contiguous; a multiple of 8 */
+  int64_t page_stride;   /* elements between pages of either cache; 0: contiguous; a multiple of head_dim */
   const int32_t* block_table; /* device [B, max_pages] */
   const int32_t* q_start;     /* device [B + 1] */
   const int32_t* seq_lens;    /* device [B] */

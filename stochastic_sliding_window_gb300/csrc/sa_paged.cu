@@ -362,9 +362,12 @@ static sa_status_t check_sizes(const sa_paged_params_t* p, Path path) {
   const long long page_elems = (long long)p->page_size * p->num_kv_heads * p->head_dim;
   if ((p->q_stride != 0 && p->q_stride < row) || p->q_stride % 8 != 0)
     return fail(SA_ERR_INVALID_ARG, "q_stride must be 0, or a multiple of 8 and at least %lld", row);
-  if ((p->page_stride != 0 && p->page_stride < page_elems) || p->page_stride % 8 != 0)
-    return fail(SA_ERR_INVALID_ARG, "page_stride must be 0, or a multiple of 8 and at least %lld",
+  if ((p->page_stride != 0 && p->page_stride < page_elems) || p->page_stride % p->head_dim != 0)
+    return fail(SA_ERR_INVALID_ARG, "page_stride must be 0, or a multiple of head_dim and at least %lld",
                 page_elems);
+  const double stride = double(p->page_stride ? p->page_stride : page_elems);
+  if (stride / p->head_dim * p->num_pages >= 4294967295.0)
+    return fail(SA_ERR_UNSUPPORTED, "a cache of more than 2^32 rows of head_dim");
   if (double(p->tokens) * p->num_q_heads >= 2147483647.0)
     return fail(SA_ERR_UNSUPPORTED, "tokens * num_q_heads too large");
   if (path != kPathSWA) {

@@ -30,20 +30,35 @@
 namespace sa {
 namespace prow {
 
-constexpr int kStages = 3;
-constexpr int kMetaInts = 32;  // 16 key tokens, then the fields below
-enum : int { kFlags = 16, kPos0, kRows, kTok0, kHr };
+// Two stages a warp and eleven warps (d = 128) beat three and seven, or four
+// and five: 621, 649 and 652 us for a decoding batch of 48 requests of up to
+// 32768 tokens (3.85 GB; 32 / 8 heads).  A warp spends its time on its own
+// instructions, not on waiting for its loads.
+constexpr int kStages = 2;
+// A stage: 16 K rows, 16 V rows, the unit's Q rows, 16 key tokens and a word of flags.
+constexpr int kMetaInts = 32;
 enum : int {
-  kFirst = 1,     // first tile of a piece (a unit's run of one path): reset O, m, l
-  kLast = 2,      // last tile of the piece: write it
-  kNewQ = 4,      // first tile of the unit here: the stage holds its Q rows
-  kIsSwa = 8,     // the piece is of the SWA path
-  kWhole = 16,    // the whole unit is this worker's
-  kTail = 32,     // the unit starts in this worker's run (partial slot 1, else 0)
-  kAny = 64,      // some key of the tile is loaded
-  kAddSwa = 128,  // gated: the SWA term comes from swa_part
-  kNone = 256,    // no tile: the run is done
-  kRaw = 512,     // (this lane) the key is an entry of sigma not yet looked at
+  kFirst = 1,    // first tile of a piece (a unit's run of one path): reset O, m, l
+  kLast = 2,     // last tile of the piece: write it
+  kNewQ = 4,     // first tile of the unit here: the stage holds its Q rows
+  kAny = 8,      // some key of the tile is loaded
+  kClear = 16,   // every row attends to all 16 keys
+  kNone = 32,    // no tile: the run is done
+  kRaw = 64,     // (one lane) the key is an entry of sigma not yet looked at
+  kWithin = 128, // SWA: the keys lie in every row's window
+  kPieceShift = 16,
+};
+// What the pieces under way have in common, eight at most from make() to the
+// last tile's sums.
+constexpr int kPieces = 8;
+struct Piece {
+  int flags, pos0, rows, t0, hr, pad[3];
+};
+enum : int {
+  kIsSwa = 1,    // the piece is of the SWA path
+  kWhole = 2,    // the whole unit is this worker's
+  kTail = 4,     // the unit starts in this worker's run (partial slot 1, else 0)
+  kAddSwa = 8,   // gated: the SWA term comes from swa_part
 };
 
 // Where a position of the laid-out tiles lies: request, its fields, and the
@@ -103,11 +118,17 @@ __device__ __forceinline__ Place locate(const Params& P, const Scan& head, int H
   }
 }
 
-template <int D, int PATH>
-__global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(const __grid_constant__ Params P) {
+// Warps of a block: as many as shared memory and registers hold.
+__host__ __device__ constexpr int most_warps(int d, int nt) {
+  return d == 128 ? (nt == 2 ? 8 : 12) : (nt == 2 ? 12 : 16);
+}
+
+template <int D, int PATH, int NT>
+__global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
+    sa_paged_rows_kernel(const __grid_constant__ Params P) {
   constexpr int kPitch = Pitch<D>;
   constexpr int kCpr = D / 8;  // 16-byte chunks per row
-  constexpr uint32_t kOffV = kKeys * kPitch, kOffQ = 2 * kKeys * kPitch;
+  constexpr uint32_t kOffQ = 2 * kKeys * kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   // the join kernel's blocks may be put on SMs that this grid has left
@@ -116,6 +137,7 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
   uint8_t* ring = smem_raw + size_t(warp) * P.warp_bytes;
   const uint32_t sring = smem_u32(ring);
   const uint32_t off_meta = kOffQ + uint32_t(P.R) * kPitch;
+  Piece* pieces = reinterpret_cast<Piece*>(ring + kStages * P.stage_bytes);
   const int HR = P.Hkv * P.rg;
 
   // ---- this worker's run [begin, end) of all units' tiles
@@ -172,30 +194,28 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     next_unit();
   }
 
-  // ---- tiles on their way: A has its page ids, B its key tokens
-  struct Tile {
-    int flags, pos0, rows, t0, hr, b, tok;  // tok: this lane's key (lane & 15), -1: none
-  };
-  int upos0 = 0, urows = 0, ut0 = 0, slo = 0, shi = 0, wlo = 0, whi = 0;
-  int have_b = -1, have_grp = -1;
-  bool fresh = true;  // the cursor's unit has not been entered yet
-  auto make = [&]() -> Tile {
-    Tile t;
-    t.tok = -1;
-    t.flags = kNone;
-    t.pos0 = t.rows = t.t0 = t.hr = t.b = 0;
+  // ---- pieces: the cursor's unit, path by path
+  int piece = -1, left = 0;          // tiles of the piece still to be made
+  int kcur = 0, khi = 0;             // next key (a position, or one of sigma's), end
+  int upos0 = 0, ulast = 0, urows = 0, ut0 = 0, slo = 0, shi = 0, wlo = 0, whi = 0;
+  int ukvh = 0, have_b = -1, have_grp = -1, first_flags = 0;
+  bool fresh = true, swa = PATH == kPathSWA;
+  auto next_piece = [&]() {
+    if (piece >= 0 && ctile == cr.tsa + cr.tsw) {
+      next_unit();
+      fresh = true;
+    }
+    if (done || (snap ? (ctile == 0 && cpos >= end) : cpos >= end)) return false;
     const int per_unit = cr.tsa + cr.tsw;
-    if (done || (snap ? (ctile == 0 && cpos >= end) : cpos >= end)) return t;
-    int flags = 0;
     if (fresh) {
       const int i0 = cgrp * P.tb, nt = min(P.tb, cr.n - i0);
       upos0 = cr.len - cr.n + i0;
+      ulast = upos0 + nt - 1;
       ut0 = cr.q0 + i0;
-      urows = P.rg > 1 ? min(16, P.g - (chr_ % P.rg) * 16) : nt * P.g;
-      if (PATH != kPathSA) {
-        wlo = max(0, upos0 - P.w + 1);
-        whi = upos0 + nt;
-      }
+      ukvh = chr_ / P.rg;
+      urows = P.rg > 1 ? min(16, P.g - (chr_ - ukvh * P.rg) * 16) : nt * P.g;
+      wlo = max(0, upos0 - P.w + 1);
+      whi = ulast + 1;
       if (PATH != kPathSWA && (have_b != cb || have_grp != cgrp)) {  // one token's heads share it
         have_b = cb;
         have_grp = cgrp;
@@ -208,61 +228,80 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
           atomicOr(P.err, SA_ERRBIT_RANGE);
         }
       }
-      flags |= kNewQ;
     }
+    swa = PATH == kPathSWA || (PATH == kPathGated && ctile >= cr.tsa);
+    const int path_end = swa ? per_unit : cr.tsa;
     const long long ustart = cpos - ctile;
     const bool whole = snap || (ustart >= begin && ustart + per_unit <= end);
-    if (whole) flags |= kWhole;
-    if (ustart >= begin) flags |= kTail;
-    if (fresh && !whole && ustart >= begin && lane == 0) {
-      Desc d;
-      d.valid = 1;
-      d.t0 = ut0;
-      d.hr = chr_;
-      d.nrows = urows;
-      d.tsa = cr.tsa;
-      d.tsw = cr.tsw;
-      d.add_swa = PATH == kPathGated && cr.tsw == 0;
-      d.pad = 0;
-      d.u0 = ustart;
-      d.per = per;
-      P.desc[worker] = d;
+    left = snap ? path_end - ctile : int(min((long long)(path_end - ctile), end - cpos));
+    const int pt = swa ? ctile - cr.tsa : ctile;
+    kcur = (swa ? wlo : slo) + pt * kKeys;
+    khi = swa ? whi : shi;
+    ++piece;
+    if (lane == 0) {
+      Piece pc;
+      pc.flags = (swa ? kIsSwa : 0) | (whole ? kWhole : 0) | (ustart >= begin ? kTail : 0) |
+                 (PATH == kPathGated && cr.tsw == 0 ? kAddSwa : 0);
+      pc.pos0 = upos0;
+      pc.rows = urows;
+      pc.t0 = ut0;
+      pc.hr = chr_;
+      pc.pad[0] = pc.pad[1] = pc.pad[2] = 0;
+      pieces[piece % kPieces] = pc;
+      if (fresh && !whole && ustart >= begin) {
+        Desc d;
+        d.valid = 1;
+        d.t0 = ut0;
+        d.hr = chr_;
+        d.nrows = urows;
+        d.tsa = cr.tsa;
+        d.tsw = cr.tsw;
+        d.add_swa = PATH == kPathGated && cr.tsw == 0;
+        d.pad = 0;
+        d.u0 = ustart;
+        d.per = per;
+        P.desc[worker] = d;
+      }
     }
-    const bool is_swa = PATH == kPathSWA || (PATH == kPathGated && ctile >= cr.tsa);
-    const int pt = is_swa ? ctile - cr.tsa : ctile;  // tile within the path
-    if (pt == 0 || fresh) flags |= kFirst;
-    if (is_swa) flags |= kIsSwa;
-    if (PATH == kPathGated && cr.tsw == 0) flags |= kAddSwa;
-    const bool path_end = ctile == (is_swa ? per_unit : cr.tsa) - 1;
-    if (path_end || (!snap && cpos == end - 1)) flags |= kLast;
-    // this lane's key
-    const int key = pt * kKeys + (lane & 15);
-    if (is_swa) {
-      const int j = wlo + key;
-      if (j < whi) t.tok = j;
-    } else {
-      const int j = slo + key;
-      if (j < shi) t.tok = P.perm[(long long)cb * P.perm_stride + j];
-      flags |= j < shi ? kRaw : 0;
-    }
-    t.flags = flags;
-    t.pos0 = upos0;
-    t.rows = urows;
-    t.t0 = ut0;
-    t.hr = chr_;
-    t.b = cb;
+    first_flags = kFirst | (fresh ? kNewQ : 0);
     fresh = false;
-    ++cpos;
-    if (++ctile == per_unit) {
-      next_unit();
-      fresh = true;
+    cpos += left;
+    ctile += left;
+    return true;
+  };
+
+  // ---- tiles on their way: A has its page ids, B its key tokens
+  struct Tile {
+    int flags, tok, b, kvh, pos0;  // tok: this lane's key (lane & 15), -1: none
+  };
+  auto make = [&]() -> Tile {
+    Tile t;
+    t.tok = -1;
+    t.flags = kNone;
+    t.b = t.kvh = t.pos0 = 0;
+    if (left == 0 && !next_piece()) return t;
+    int flags = first_flags | (piece % kPieces) << kPieceShift;
+    first_flags = 0;
+    if (--left == 0) flags |= kLast;
+    const int key = kcur + (lane & 15);
+    if (swa) {
+      if (kcur + kKeys - 1 <= upos0 && ulast - kcur < P.w) flags |= kWithin;
+      if (key < khi) t.tok = key;
+    } else if (key < khi) {
+      t.tok = P.perm[(long long)cb * P.perm_stride + key];
+      flags |= kRaw;
     }
+    kcur += kKeys;
+    t.flags = flags;
+    t.b = cb;
+    t.kvh = ukvh;
+    t.pos0 = upos0;
     return t;
   };
   // sigma's entries are looked at a step after their loads began
   auto settle = [&](Tile& t) {
     if (PATH == kPathSWA || !(t.flags & kRaw)) return;
-    t.flags &= ~kRaw;
+    t.flags = (t.flags & ~kRaw) | kWithin;
     if (unsigned(t.tok) >= unsigned(P.perm_len)) {
       atomicOr(P.err, SA_ERRBIT_RANGE);
       t.tok = -1;
@@ -271,54 +310,38 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     }
   };
   auto page_of = [&](const Tile& t) {  // -1: no key
-    return t.tok >= 0 ? P.table[(long long)t.b * P.max_pages + int(unsigned(t.tok) / unsigned(P.page))] : -1;
+    return t.tok >= 0 ? P.table[(long long)t.b * P.max_pages + page_col(P, t.tok)] : -1;
   };
   auto issue = [&](const Tile& t, int page, int stage) {
     uint8_t* st = ring + uint32_t(stage) * P.stage_bytes;
     const uint32_t ss = sring + uint32_t(stage) * P.stage_bytes;
     int* meta = reinterpret_cast<int*>(st + off_meta);
     if (t.flags & kNone) {
-      if (lane == 0) meta[kFlags] = kNone;
+      if (lane == 0) meta[kKeys] = kNone;
       return;
     }
-    const int kvh = t.hr / P.rg;
-    long long off = -1;
+    uint32_t row = 0xffffffffu;
     if (t.tok >= 0) {
-      if (unsigned(page) < unsigned(P.num_pages)) {
-        const int in = int(unsigned(t.tok) % unsigned(P.page));
-        off = (long long)page * P.page_stride + ((long long)in * P.Hkv + kvh) * D;
-      } else {
+      if (unsigned(page) < unsigned(P.num_pages))
+        row = uint32_t(page) * uint32_t(P.page_rows) + uint32_t(page_in(P, t.tok)) * uint32_t(P.Hkv) + uint32_t(t.kvh);
+      else
         atomicOr(P.err, SA_ERRBIT_RANGE);
-      }
     }
-    const bool any = __any_sync(0xffffffffu, off >= 0);
-    if (lane < kKeys) meta[lane] = off >= 0 ? t.tok : 0x7fffffff;
-    if (lane == 0) {
-      meta[kFlags] = t.flags | (any ? kAny : 0);
-      meta[kPos0] = t.pos0;
-      meta[kRows] = t.rows;
-      meta[kTok0] = t.t0;
-      meta[kHr] = t.hr;
-    }
-    if (any) {
-      const int c = lane % kCpr;
-#pragma unroll
-      for (int i = 0; i < kKeys * kCpr / 32; ++i) {
-        const int row = i * (32 / kCpr) + lane / kCpr;
-        const long long o = __shfl_sync(0xffffffffu, off, row);
-        const int bytes = o >= 0 ? 16 : 0;  // rows without a key are filled with zeros
-        const long long at = (o >= 0 ? o : 0) + c * 8;
-        cp_async16_zfill(ss + row * kPitch + c * 16, P.k + at, bytes);
-        cp_async16_zfill(ss + kOffV + row * kPitch + c * 16, P.v + at, bytes);
-      }
-    }
+    const unsigned have = __ballot_sync(0xffffffffu, row != 0xffffffffu);
+    const bool clear = __all_sync(0xffffffffu, row != 0xffffffffu && (t.flags & kWithin));
+    if (lane < kKeys) meta[lane] = row != 0xffffffffu ? t.tok : 0x7fffffff;
+    if (lane == 0) meta[kKeys] = (t.flags & ~kRaw) | (have != 0u ? kAny : 0) | (clear ? kClear : 0);
+    if (have != 0u) load_tile<D>(P.k, P.v, ss, row);
     if (t.flags & kNewQ) {
-      const int h0 = kvh * P.g + (P.rg > 1 ? (t.hr - kvh * P.rg) * 16 : 0);
-      for (int i = lane; i < t.rows * kCpr; i += 32) {
+      __syncwarp();
+      const Piece* pc = pieces + ((t.flags >> kPieceShift) & (kPieces - 1));
+      const int rows = pc->rows, t0 = pc->t0;
+      const int h0 = t.kvh * P.g + (P.rg > 1 ? (pc->hr - t.kvh * P.rg) * 16 : 0);
+      for (int i = lane; i < rows * kCpr; i += 32) {
         const int r = i / kCpr, c = i - r * kCpr;
         const int tk = P.rg > 1 ? 0 : r / P.g;
         cp_async16(ss + kOffQ + r * kPitch + c * 16,
-                   P.q + (long long)(t.t0 + tk) * P.q_stride + (h0 + r - tk * P.g) * D + c * 8);
+                   P.q + (long long)(t0 + tk) * P.q_stride + (h0 + r - tk * P.g) * D + c * 8);
       }
     }
   };
@@ -336,18 +359,15 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     pa = page_of(ta);
     tn = make();
   };
-  step(0);
-  step(1);
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) step(i);
 
-  uint32_t qf[D / 16][4];
-  Acc<D> acc;
-  float (&o)[D / 8][4] = acc.o;
-  float &m0 = acc.m0, &m1 = acc.m1, &l0 = acc.l0, &l1 = acc.l1;
-  float stash[PATH == kPathGated ? D / 8 : 1][4];
+  Acc<D, NT> acc;
+  float stash[PATH == kPathGated ? D / 16 : 1][NT][4];
   acc.reset();
-  const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows of the unit
-  const int rt0 = P.rg > 1 ? 0 : r0 / P.g, rt1 = P.rg > 1 ? 0 : r1 / P.g;
   int stage = 0, fill = kStages - 1;
+  int pflags = 0, rows = 0, t0 = 0, h0 = 0;
+  unsigned w = 0;
   while (true) {
     step(fill);
     fill = fill + 1 == kStages ? 0 : fill + 1;
@@ -356,80 +376,60 @@ __global__ void __launch_bounds__(D == 128 ? 256 : 512, 1) sa_paged_rows_kernel(
     uint8_t* st = ring + uint32_t(stage) * P.stage_bytes;
     const uint32_t ss = sring + uint32_t(stage) * P.stage_bytes;
     const int* meta = reinterpret_cast<const int*>(st + off_meta);
-    const int flags = meta[kFlags];
+    const int flags = meta[kKeys];
     if (flags & kNone) break;
-    const int pos0 = meta[kPos0], rows = meta[kRows];
     if (flags & kFirst) {
+      const Piece* pc = pieces + ((flags >> kPieceShift) & (kPieces - 1));
+      pflags = pc->flags;
+      rows = pc->rows;
+      t0 = pc->t0;
+      const int hr = pc->hr, kvh = hr / P.rg;
+      h0 = kvh * P.g + (P.rg > 1 ? (hr - kvh * P.rg) * 16 : 0);
+      w = pflags & kIsSwa ? unsigned(P.w) : 0x7fffffffu;
       acc.reset();
+      if (flags & kNewQ) acc.rows_of(ss + kOffQ, rows, pc->pos0, P.g, P.rg > 1);
     }
-    if (flags & kNewQ) {
-      load_q<D>(ss + kOffQ, rows, qf);
-    }
-    if (flags & kAny) {
-      const unsigned w = PATH == kPathSWA || (flags & kIsSwa) ? unsigned(P.w) : 0x7fffffffu;
-      const int p0 = r0 < rows ? pos0 + rt0 : -1, p1 = r1 < rows ? pos0 + rt1 : -1;
-      acc.tile(ss, ss + kOffV, meta, qf, p0, p1, w, P.scale_log2);
-    }
+    if (flags & kAny) acc.tile(ss, meta, w, (flags & kClear) != 0, P.scale_log2);
     if (flags & kLast) {
-      const int t0 = meta[kTok0], hr = meta[kHr];
-      const int kvh = hr / P.rg;
-      const int h0 = kvh * P.g + (P.rg > 1 ? (hr - kvh * P.rg) * 16 : 0);
       acc.sum_rows();
-      if (!(flags & kWhole)) {
-        const int slot = (worker * 2 + ((flags & kTail) ? 1 : 0)) * (PATH == kPathGated ? 2 : 1) +
-                         (PATH == kPathGated && (flags & kIsSwa) ? 1 : 0);
+      if (!(pflags & kWhole)) {
+        const int slot = (worker * 2 + ((pflags & kTail) ? 1 : 0)) * (PATH == kPathGated ? 2 : 1) +
+                         (PATH == kPathGated && (pflags & kIsSwa) ? 1 : 0);
         acc.write(P.part + size_t(slot) * P.slot_floats, P.R, rows);
       } else {
-        float f0 = l0 == 0.f ? 0.f : 1.f / l0, f1 = l1 == 0.f ? 0.f : 1.f / l1;
-        const size_t row0 = size_t(t0 + rt0) * P.Hq + h0 + r0 - rt0 * P.g;
-        const size_t row1 = size_t(t0 + rt1) * P.Hq + h0 + r1 - rt1 * P.g;
-        bool write = true;
-        if (PATH == kPathGated) {
-          const float* gate = (flags & kIsSwa) ? P.gate_swa : P.gate_sa;
-          if (r0 < rows) f0 *= 1.f / (1.f + expf(-gate[row0]));
-          if (r1 < rows) f1 *= 1.f / (1.f + expf(-gate[row1]));
-          write = (flags & (kIsSwa | kAddSwa)) != 0;
-          if (flags & kIsSwa) {
+        const bool write = PATH != kPathGated || (pflags & (kIsSwa | kAddSwa)) != 0;
+        uint8_t* os = st + kOffQ;  // this stage's Q rows, whose fragments were taken
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][0] = fmaf(o[i][0], f0, stash[i][0]);
-              o[i][1] = fmaf(o[i][1], f0, stash[i][1]);
-              o[i][2] = fmaf(o[i][2], f1, stash[i][2]);
-              o[i][3] = fmaf(o[i][3], f1, stash[i][3]);
-            }
-            f0 = f1 = 1.f;
-          } else if (!write) {
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              stash[i][0] = o[i][0] * f0;
-              stash[i][1] = o[i][1] * f0;
-              stash[i][2] = o[i][2] * f1;
-              stash[i][3] = o[i][3] * f1;
-            }
-          } else {
+          for (int e = 0; e < 2; ++e) {
+            const int r = t * 8 + 2 * (lane & 3) + e;
+            const int tk = P.rg > 1 ? 0 : r / P.g;
+            const size_t orow = size_t(t0 + tk) * P.Hq + h0 + r - tk * P.g;
+            float f = acc.l[t][e] == 0.f ? 0.f : 1.f / acc.l[t][e];
+            if (PATH == kPathGated && r < rows)
+              f *= 1.f / (1.f + expf(-((pflags & kIsSwa) ? P.gate_swa : P.gate_sa)[orow]));
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const int c = i * 8 + (lane & 3) * 2;
-              const float2 z = make_float2(0.f, 0.f);
-              const float2 a = r0 < rows ? *reinterpret_cast<const float2*>(P.swa_part + row0 * D + c) : z;
-              const float2 b = r1 < rows ? *reinterpret_cast<const float2*>(P.swa_part + row1 * D + c) : z;
-              o[i][0] = fmaf(o[i][0], f0, a.x);
-              o[i][1] = fmaf(o[i][1], f0, a.y);
-              o[i][2] = fmaf(o[i][2], f1, b.x);
-              o[i][3] = fmaf(o[i][3], f1, b.y);
+            for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float y = acc.o[i][t][2 * h + e] * f;
+                const int col = i * 16 + (lane >> 2) + 8 * h;
+                if (PATH == kPathGated) {
+                  if (pflags & kIsSwa)
+                    y += stash[i][t][2 * h + e];
+                  else if (!write)
+                    stash[i][t][2 * h + e] = y;
+                  else if (r < rows)
+                    y += P.swa_part[orow * D + col];
+                }
+                if (write && r < rows)
+                  *reinterpret_cast<__nv_bfloat16*>(os + r * kPitch + col * 2) = __float2bfloat16_rn(y);
+              }
             }
-            f0 = f1 = 1.f;
           }
         }
         if (write) {
-          // through this stage's Q rows, whose fragments were taken, to whole 16-byte stores
-          uint8_t* os = st + kOffQ;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const int c = (i * 8 + (lane & 3) * 2) * 2;
-            if (r0 < rows) *reinterpret_cast<uint32_t*>(os + r0 * kPitch + c) = pack_bf16x2(o[i][0] * f0, o[i][1] * f0);
-            if (r1 < rows) *reinterpret_cast<uint32_t*>(os + r1 * kPitch + c) = pack_bf16x2(o[i][2] * f1, o[i][3] * f1);
-          }
           __syncwarp();
           for (int i = lane; i < rows * kCpr; i += 32) {
             const int r = i / kCpr, c = i - r * kCpr;
@@ -520,10 +520,9 @@ static Config make_config(const PagedProblem& pb, Path path, int row_limit, int 
   c.slot_floats = (c.R * (pb.d + 2) + 3) / 4 * 4;  // 16-byte aligned slots
   const uint32_t pitch = uint32_t(pb.d) * 2 + 16;
   c.stage_bytes = (2 * kKeys + uint32_t(c.R)) * pitch + kMetaInts * 4;
-  c.warp_bytes = c.stage_bytes * kStages;
+  c.warp_bytes = c.stage_bytes * kStages + kPieces * uint32_t(sizeof(Piece));
   c.warps = int(kMaxSmem / c.warp_bytes);
-  const int most_warps = pb.d == 128 ? 8 : 16;
-  if (c.warps > most_warps) c.warps = most_warps;
+  c.warps = min(c.warps, most_warps(pb.d, c.R > 8 ? 2 : 1));
   c.workers = sms * c.warps;
   // Short units are left whole where there are at least four for each worker.
   const long long units = (pb.T + c.tb - 1) / c.tb * (long long)pb.Hkv * c.rg;
@@ -534,13 +533,19 @@ static Config make_config(const PagedProblem& pb, Path path, int row_limit, int 
   return c;
 }
 
+template <int D, int PATH, int NT>
+static cudaError_t launch_rows(const Params& P, const Config& c, int sms, cudaStream_t stream) {
+  const uint32_t smem = c.warp_bytes * uint32_t(c.warps);
+  const cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH, NT>>(kMaxSmem);
+  if (ce != cudaSuccess) return ce;
+  sa_paged_rows_kernel<D, PATH, NT><<<sms, 32 * c.warps, smem, stream>>>(P);
+  return cudaGetLastError();
+}
+
 template <int D, int PATH>
 static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStream_t stream) {
-  const uint32_t smem = c.warp_bytes * uint32_t(c.warps);
-  cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH>>(kMaxSmem);
-  if (ce != cudaSuccess) return ce;
-  sa_paged_rows_kernel<D, PATH><<<sms, 32 * c.warps, smem, stream>>>(P);
-  if ((ce = cudaGetLastError()) != cudaSuccess || c.snap) return ce;
+  const cudaError_t ce = c.R <= 8 ? launch_rows<D, PATH, 1>(P, c, sms, stream) : launch_rows<D, PATH, 2>(P, c, sms, stream);
+  if (ce != cudaSuccess || c.snap) return ce;
   // its blocks may be set up while the row kernel's last ones finish
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(c.workers));
@@ -571,7 +576,10 @@ void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, 
   P.out = static_cast<__nv_bfloat16*>(pb.out);
   P.err = pb.err;
   P.q_stride = pb.q_stride;
-  P.page_stride = pb.page_stride;
+  P.page_rows = int(pb.page_stride / pb.d);
+  P.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (pb.page == 1 << i) P.page_shift = i;
   P.perm_stride = pb.perm_rows == 1 ? 0 : pb.perm_len;
   P.B = pb.B;
   P.T = pb.T;

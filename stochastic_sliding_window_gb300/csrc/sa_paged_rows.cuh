@@ -36,8 +36,9 @@ struct Params {
   int32_t* err;
   float* part;            // partial slots, then Desc[workers]; nullptr: never split
   Desc* desc;
-  long long q_stride, page_stride, perm_stride;
-  int B, T, max_new, row_limit, Hq, Hkv, g, page, num_pages, max_pages;
+  long long q_stride, perm_stride;
+  int B, T, max_new, row_limit, Hq, Hkv, g, page, page_shift, num_pages, max_pages;
+  int page_rows;          // rows of D elements between pages
   int w, half, perm_len;
   int tb, rg, R;          // tokens and rows of a unit; row groups of a kv head (g > 16)
   int slot_floats;        // one partial: O [R, D], then (m, l) [R]; a multiple of 4
@@ -101,139 +102,231 @@ __device__ __forceinline__ Request load_request(const Params& P, int b, bool rep
 template <int D>
 constexpr int Pitch = D * 2 + 16;
 
-// A fragments of a unit's query rows.  Rows past the last read the first:
-// their weights are all masked.
-template <int D>
-__device__ __forceinline__ void load_q(uint32_t sq, int rows, uint32_t (&qf)[D / 16][4]) {
-  const int lane = threadIdx.x & 31;
-  int r = (lane & 7) + ((lane >> 3) & 1) * 8;
-  if (r >= rows) r = 0;
-  const uint32_t a = sq + r * Pitch<D> + (lane >> 4) * 16;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) ldsm4(a + i * 32, qf[i]);
+// Page and row of a position (page_shift: log2 of a page size that is a power
+// of two, else -1).
+__device__ __forceinline__ int page_col(const Params& P, int tok) {
+  return P.page_shift >= 0 ? tok >> P.page_shift : int(unsigned(tok) / unsigned(P.page));
+}
+__device__ __forceinline__ int page_in(const Params& P, int tok) {
+  return P.page_shift >= 0 ? tok & (P.page - 1) : int(unsigned(tok) % unsigned(P.page));
 }
 
-// A warp's running softmax of 16 rows: this lane's rows are lane / 4 and
-// lane / 4 + 8, its columns 8 i + 2 (lane % 4) and the next.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Loads 16 keys' rows of K and V (row numbers of D elements in lanes 0-15,
+// 0xffffffff: none, filled with zeros) into a stage.
 template <int D>
+__device__ __forceinline__ void load_tile(const __nv_bfloat16* k, const __nv_bfloat16* v, uint32_t stage,
+                                          uint32_t row) {
+  constexpr int kCpr = D / 8;
+  const int lane = threadIdx.x & 31, c = lane % kCpr;
+  const uint32_t dst = stage + (lane / kCpr) * Pitch<D> + c * 16;
+  const char* kc = reinterpret_cast<const char*>(k + c * 8);
+  const char* vc = reinterpret_cast<const char*>(v + c * 8);
+  if (__all_sync(0xffffffffu, row != 0xffffffffu)) {
+#pragma unroll
+    for (int i = 0; i < kKeys * kCpr / 32; ++i) {
+      const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / kCpr) + lane / kCpr);
+      const uint64_t at = uint64_t(r) * uint32_t(D * 2);
+      cp_async16(dst + i * (32 / kCpr) * Pitch<D>, kc + at);
+      cp_async16(dst + (kKeys + i * (32 / kCpr)) * Pitch<D>, vc + at);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeys * kCpr / 32; ++i) {
+      const uint32_t r = __shfl_sync(0xffffffffu, row, i * (32 / kCpr) + lane / kCpr);
+      const int bytes = r != 0xffffffffu ? 16 : 0;
+      const uint64_t at = uint64_t(r != 0xffffffffu ? r : 0u) * uint32_t(D * 2);
+      cp_async16_zfill(dst + i * (32 / kCpr) * Pitch<D>, kc + at, bytes);
+      cp_async16_zfill(dst + (kKeys + i * (32 / kCpr)) * Pitch<D>, vc + at, bytes);
+    }
+  }
+}
+
+// A warp's running softmax of 8 NT query rows.  Both products are taken
+// transposed, so that the 16 of the matrix instruction's M are keys, then
+// columns of O, and its 8 of N are query rows -- a unit of up to 8 rows (any
+// decoding with up to 8 query heads per kv head) wastes nothing:
+//   S^T [16 keys, 8 rows] = K Q^T,   O^T [D, 8 rows] += V^T P^T.
+// This lane's rows are 8 nt + 2 (lane % 4) + {0, 1}; its keys lane / 4 and
+// lane / 4 + 8; its columns of O 16 i + lane / 4 and 8 more.  P turns from the
+// first product's result layout to the second's operand layout by a transpose
+// of 8 x 8 blocks in registers.
+template <int D, int NT>
 struct Acc {
-  float o[D / 8][4];
-  float m0, m1, l0, l1;  // maxima in log2 units; the sums are this lane's share
+  uint32_t qf[D / 16][NT][2];  // Q^T fragments
+  float o[D / 16][NT][4];
+  float m[NT][2], l[NT][2];    // maxima in log2 units; sums: this lane's share
+  int pos[NT][2];              // the rows' positions (-1: no row)
 
   __device__ __forceinline__ void reset() {
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
+    }
   }
 
-  // 16 keys: K rows at sk, V rows at sv, their tokens in tok (0x7fffffff: no
-  // key).  p0, p1: the positions of this lane's rows (-1: no row); a row
-  // attends to tokens p - w + 1 .. p.
-  __device__ __forceinline__ void tile(uint32_t sk, uint32_t sv, const int* toks,
-                                       const uint32_t (&qf)[D / 16][4], int p0, int p1, unsigned w,
-                                       float scale_log2) {
-    constexpr int kPitch = Pitch<D>;
+  // The unit's rows: Q at sq; row r is of the token r / g (of the one token
+  // where a unit holds one) from position pos0 on.  Rows past the last read
+  // the first: all their weights are masked.
+  __device__ __forceinline__ void rows_of(uint32_t sq, int rows, int pos0, int g, bool one) {
     const int lane = threadIdx.x & 31;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      int r = t * 8 + (lane & 7);
+      if (r >= rows) r = 0;
+      const uint32_t a = sq + r * Pitch<D> + (lane >> 3) * 16;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t f[4];
+        ldsm4(a + i * 64, f);
+        qf[2 * i][t][0] = f[0];
+        qf[2 * i][t][1] = f[1];
+        qf[2 * i + 1][t][0] = f[2];
+        qf[2 * i + 1][t][1] = f[3];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = t * 8 + 2 * (lane & 3) + e;
+        pos[t][e] = row < rows ? pos0 + (one ? 0 : row / g) : -1;
+      }
+    }
+  }
+
+  // 16 keys: K rows at sk, V rows behind them, their tokens in toks
+  // (0x7fffffff: no key); a row attends to tokens p - w + 1 .. p of its
+  // position p.  clear: every real row attends to all of them.
+  __device__ __forceinline__ void tile(uint32_t sk, const int* toks, unsigned w, bool clear, float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
     {
-      const uint32_t a = sk + ((lane & 7) + (lane >> 4) * 8) * kPitch + ((lane >> 3) & 1) * 16;
+      const uint32_t a = sk + ((lane & 7) + ((lane >> 3) & 1) * 8) * Pitch<D> + (lane >> 4) * 16;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t kf[4];
         ldsm4(a + i * 32, kf);
-        mma16816(s[0], qf[i], kf[0], kf[1]);
-        mma16816(s[1], qf[i], kf[2], kf[3]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816(s[t], kf, qf[i][t][0], qf[i][t][1]);
       }
     }
-    float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int2 tok = *reinterpret_cast<const int2*>(toks + t * 8 + (lane & 3) * 2);
-      s[t][0] = unsigned(p0 - tok.x) < w ? s[t][0] * scale_log2 : -INFINITY;
-      s[t][1] = unsigned(p0 - tok.y) < w ? s[t][1] * scale_log2 : -INFINITY;
-      s[t][2] = unsigned(p1 - tok.x) < w ? s[t][2] * scale_log2 : -INFINITY;
-      s[t][3] = unsigned(p1 - tok.y) < w ? s[t][3] * scale_log2 : -INFINITY;
-      x0 = fmax3(x0, s[t][0], s[t][1]);
-      x1 = fmax3(x1, s[t][2], s[t][3]);
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] *= scale_log2;
     }
+    if (!clear) {
+      const int ta = toks[lane >> 2], tb = toks[(lane >> 2) + 8];
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-    }
-    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
-      const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= a0;
-      l1 *= a1;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= a0;
-        o[i][1] *= a0;
-        o[i][2] *= a1;
-        o[i][3] *= a1;
+      for (int t = 0; t < NT; ++t) {
+        if (unsigned(pos[t][0] - ta) >= w) s[t][0] = -INFINITY;
+        if (unsigned(pos[t][1] - ta) >= w) s[t][1] = -INFINITY;
+        if (unsigned(pos[t][0] - tb) >= w) s[t][2] = -INFINITY;
+        if (unsigned(pos[t][1] - tb) >= w) s[t][3] = -INFINITY;
       }
     }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-    uint32_t hi[4], lo[4];
+    float x[NT][2];
+    bool up = false;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float e0 = fast_exp2(s[t][0] - b0), e1 = fast_exp2(s[t][1] - b0);
-      const float e2 = fast_exp2(s[t][2] - b1), e3 = fast_exp2(s[t][3] - b1);
-      l0 += e0 + e1;
-      l1 += e2 + e3;
-      hi[2 * t] = pack_bf16x2(e0, e1);
-      hi[2 * t + 1] = pack_bf16x2(e2, e3);
-      lo[2 * t] = pack_bf16x2(e0 - __uint_as_float(hi[2 * t] << 16), e1 - __uint_as_float(hi[2 * t] & 0xffff0000u));
-      lo[2 * t + 1] = pack_bf16x2(e2 - __uint_as_float(hi[2 * t + 1] << 16),
-                                  e3 - __uint_as_float(hi[2 * t + 1] & 0xffff0000u));
+    for (int t = 0; t < NT; ++t) {
+      x[t][0] = fmaxf(s[t][0], s[t][2]);
+      x[t][1] = fmaxf(s[t][1], s[t][3]);
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) {
+        x[t][0] = fmaxf(x[t][0], __shfl_xor_sync(0xffffffffu, x[t][0], d));
+        x[t][1] = fmaxf(x[t][1], __shfl_xor_sync(0xffffffffu, x[t][1], d));
+      }
+      up = up || x[t][0] > m[t][0] || x[t][1] > m[t][1];
     }
-    const uint32_t a = sv + ((lane & 7) + ((lane >> 3) & 1) * 8) * kPitch + (lane >> 4) * 16;
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float n = fmaxf(m[t][e], x[t][e]);
+          f[e] = m[t][e] == -INFINITY ? 0.f : fast_exp2(m[t][e] - n);
+          m[t][e] = n;
+          l[t][e] *= f[e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][t][0] *= f[0];
+          o[i][t][1] *= f[1];
+          o[i][t][2] *= f[0];
+          o[i][t][3] *= f[1];
+        }
+      }
+    }
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = fast_exp2(s[t][2 * h] - b0), p1 = fast_exp2(s[t][2 * h + 1] - b1);
+        l[t][0] += p0;
+        l[t][1] += p1;
+        const uint32_t a = pack_bf16x2(p0, p1);
+        hi[t][h] = transpose8(a);
+        lo[t][h] = transpose8(pack_bf16x2(p0 - __uint_as_float(a << 16), p1 - __uint_as_float(a & 0xffff0000u)));
+      }
+    }
+    const uint32_t a = sk + (kKeys + (lane & 7) + (lane >> 4) * 8) * Pitch<D> + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t vf[4];
       ldsm4t(a + i * 32, vf);
-      mma16816(o[2 * i], hi, vf[0], vf[1]);
-      mma16816(o[2 * i + 1], hi, vf[2], vf[3]);
-      mma16816(o[2 * i], lo, vf[0], vf[1]);
-      mma16816(o[2 * i + 1], lo, vf[2], vf[3]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma16816(o[i][t], vf, hi[t][0], hi[t][1]);
+        mma16816(o[i][t], vf, lo[t][0], lo[t][1]);
+      }
     }
   }
 
   // The lanes' shares of the rows' sums to every lane of the row.
   __device__ __forceinline__ void sum_rows() {
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) {
+        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], d);
+        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], d);
+      }
     }
   }
 
   // O [R, D], then (m, l) [R], of the first `rows` rows.
   __device__ __forceinline__ void write(float* pw, int R, int rows) const {
     const int lane = threadIdx.x & 31;
-    const int r0 = lane >> 2, r1 = r0 + 8;
-    if (r0 < rows) {
-      if ((lane & 3) == 0) {
-        pw[R * D + 2 * r0] = m0;
-        pw[R * D + 2 * r0 + 1] = l0;
-      }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(pw + r0 * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][0], o[i][1]);
-    }
-    if (r1 < rows) {
-      if ((lane & 3) == 0) {
-        pw[R * D + 2 * r1] = m1;
-        pw[R * D + 2 * r1 + 1] = l1;
-      }
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(pw + r1 * D + i * 8 + (lane & 3) * 2) = make_float2(o[i][2], o[i][3]);
+      for (int e = 0; e < 2; ++e) {
+        const int r = t * 8 + 2 * (lane & 3) + e;
+        if (r >= rows) continue;
+        if (lane < 4) {
+          pw[R * D + 2 * r] = m[t][e];
+          pw[R * D + 2 * r + 1] = l[t][e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          pw[r * D + i * 16 + (lane >> 2)] = o[i][t][e];
+          pw[r * D + i * 16 + (lane >> 2) + 8] = o[i][t][2 + e];
+        }
+      }
     }
   }
 };

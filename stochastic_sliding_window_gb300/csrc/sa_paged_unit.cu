@@ -24,7 +24,7 @@ constexpr int kUnitThreads = 32 * kUnitWarps;
 constexpr int kMostKeys = 1280;
 constexpr int kRounds = kMostKeys / kUnitThreads + 1;  // window entries per thread
 
-template <int D, int PATH>
+template <int D, int PATH, int NT>
 __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __grid_constant__ Params P) {
   constexpr int kPitch = Pitch<D>;
   constexpr int kCpr = D / 8;
@@ -32,11 +32,11 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_count[kRounds][kUnitWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // shared memory: Q rows, key offsets, key tokens, the warps' stages
+  // shared memory: Q rows, the keys' row numbers and tokens, the warps' stages
   const uint32_t off_list = uint32_t(P.R) * kPitch;
-  const uint32_t off_tok = off_list + uint32_t(P.list_keys) * 8;
+  const uint32_t off_tok = off_list + uint32_t(P.list_keys) * 4;
   const uint32_t off_ring = (off_tok + uint32_t(P.list_keys) * 4 + 127) / 128 * 128;
-  long long* list = reinterpret_cast<long long*>(smem + off_list);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + off_list);
   int* toks = reinterpret_cast<int*>(smem + off_tok);
   uint8_t* ring = smem + off_ring + uint32_t(warp) * uint32_t(P.stages) * kStageBytes;
   const uint32_t sring = smem_u32(ring);
@@ -65,15 +65,14 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
   // ---- the keys
   const int32_t* table = P.table + (long long)b * P.max_pages;
   auto place = [&](int at, int tok, int page) {  // entry `at` of the list
-    long long off = -1;
+    uint32_t row = 0xffffffffu;
     if (unsigned(page) < unsigned(P.num_pages)) {
-      const int in = int(unsigned(tok) % unsigned(P.page));
-      off = (long long)page * P.page_stride + ((long long)in * P.Hkv + kvh) * D;
+      row = uint32_t(page) * uint32_t(P.page_rows) + uint32_t(page_in(P, tok)) * uint32_t(P.Hkv) + uint32_t(kvh);
     } else {
       atomicOr(P.err, SA_ERRBIT_RANGE);
       tok = 0x7fffffff;
     }
-    list[at] = off;
+    list[at] = row;
     toks[at] = tok;
   };
   int sa_tiles = 0, sa_keys = 0;
@@ -101,7 +100,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
     int page[kRounds];
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
-      page[k] = tok[k] >= 0 ? table[unsigned(tok[k]) / unsigned(P.page)] : 0;
+      page[k] = tok[k] >= 0 ? table[page_col(P, tok[k])] : 0;
       mine[k] = __ballot_sync(0xffffffffu, tok[k] >= 0);
       if (lane == 0) s_count[k][warp] = __popc(mine[k]);
     }
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
     }
     sa_tiles = (sa_keys + kKeys - 1) / kKeys;
     if (tid < sa_tiles * kKeys - sa_keys) {
-      list[sa_keys + tid] = -1;
+      list[sa_keys + tid] = 0xffffffffu;
       toks[sa_keys + tid] = 0x7fffffff;
     }
   }
@@ -129,9 +128,9 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
     tiles += (keys + kKeys - 1) / kKeys;
     for (int k = tid; k < (tiles - sa_tiles) * kKeys; k += kUnitThreads) {
       if (k < keys) {
-        place(base + k, lo + k, table[unsigned(lo + k) / unsigned(P.page)]);
+        place(base + k, lo + k, table[page_col(P, lo + k)]);
       } else {
-        list[base + k] = -1;
+        list[base + k] = 0xffffffffu;
         toks[base + k] = 0x7fffffff;
       }
     }
@@ -140,39 +139,39 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
   __syncthreads();
 
   // ---- this warp's tiles
-  uint32_t qf[D / 16][4];
-  load_q<D>(smem_u32(smem), rows, qf);
   int issued = warp;  // next tile to load
   auto issue = [&](int stage) {
     if (issued < tiles) {
-      const uint32_t ss = sring + uint32_t(stage) * kStageBytes;
-      const int c = lane % kCpr;
-#pragma unroll
-      for (int i = 0; i < kKeys * kCpr / 32; ++i) {
-        const int row = i * (32 / kCpr) + lane / kCpr;
-        const long long o = list[issued * kKeys + row];
-        const int bytes = o >= 0 ? 16 : 0;  // rows without a key are filled with zeros
-        const long long at = (o >= 0 ? o : 0) + c * 8;
-        cp_async16_zfill(ss + row * kPitch + c * 16, P.k + at, bytes);
-        cp_async16_zfill(ss + kKeys * kPitch + row * kPitch + c * 16, P.v + at, bytes);
-      }
+      load_tile<D>(P.k, P.v, sring + uint32_t(stage) * kStageBytes, list[issued * kKeys + (lane & 15)]);
       issued += kUnitWarps;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  Acc<D> acc;
-  acc.reset();
-  float stash[PATH == kPathGated ? D / 8 : 1][4], sm0 = -INFINITY, sm1 = -INFINITY, sl0 = 0.f, sl1 = 0.f;
-  if (PATH == kPathGated) {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) stash[i][0] = stash[i][1] = stash[i][2] = stash[i][3] = 0.f;
-  }
-  const int r0 = lane >> 2, r1 = r0 + 8;
-  const int p0 = r0 < rows ? pos0 + (P.rg > 1 ? 0 : r0 / P.g) : -1;
-  const int p1 = r1 < rows ? pos0 + (P.rg > 1 ? 0 : r1 / P.g) : -1;
   for (int i = 0; i + 1 < P.stages; ++i) issue(i);
-  int stage = 0, fill = P.stages - 1;
+  Acc<D, NT> acc;
+  acc.reset();
+  acc.rows_of(smem_u32(smem), rows, pos0, P.g, P.rg > 1);
+  // gated: what the SA path left when the SWA path begins
+  float stash[PATH == kPathGated ? D / 16 : 1][NT][4], sm[NT][2], sl[NT][2];
   bool swapped = PATH != kPathGated;
+  auto swap = [&]() {
+    swapped = true;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < (PATH == kPathGated ? D / 16 : 0); ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) stash[i][n][e] = acc.o[i][n][e];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sm[n][e] = acc.m[n][e];
+        sl[n][e] = acc.l[n][e];
+      }
+    }
+    acc.reset();
+  };
+  int stage = 0, fill = P.stages - 1;
   for (int t = warp; t < tiles; t += kUnitWarps) {
     issue(fill);
     fill = fill + 1 == P.stages ? 0 : fill + 1;
@@ -181,54 +180,36 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
     else
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();
-    if (PATH == kPathGated && !swapped && t >= sa_tiles) {  // on to the SWA path
-      swapped = true;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) stash[i][e] = acc.o[i][e];
-      }
-      sm0 = acc.m0;
-      sm1 = acc.m1;
-      sl0 = acc.l0;
-      sl1 = acc.l1;
-      acc.reset();
-    }
-    const uint32_t ss = sring + uint32_t(stage) * kStageBytes;
-    acc.tile(ss, ss + kKeys * kPitch, toks + t * kKeys, qf, p0, p1, t >= sa_tiles ? unsigned(P.w) : 0x7fffffffu,
-             P.scale_log2);
+    if (!swapped && t >= sa_tiles) swap();
+    acc.tile(sring + uint32_t(stage) * kStageBytes, toks + t * kKeys, t >= sa_tiles ? unsigned(P.w) : 0x7fffffffu,
+             false, P.scale_log2);
     __syncwarp();
     stage = stage + 1 == P.stages ? 0 : stage + 1;
   }
+  if (!swapped) swap();
 
-  // ---- the warps' parts, through their stages
+  // ---- the warps' parts, through their stages (gated: SA's behind SWA's)
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   float* part = reinterpret_cast<float*>(ring);
+  acc.sum_rows();
+  acc.write(part, P.R, rows);
   if (PATH == kPathGated) {
-    // slot 0: SA, slot 1: SWA
-    Acc<D> first = acc;
-    if (swapped) {
-      acc.sum_rows();
-      acc.write(part + P.slot_floats, P.R, rows);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) first.o[i][e] = stash[i][e];
+      for (int i = 0; i < (PATH == kPathGated ? D / 16 : 0); ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc.o[i][n][e] = stash[i][n][e];
       }
-      first.m0 = sm0;
-      first.m1 = sm1;
-      first.l0 = sl0;
-      first.l1 = sl1;
-    } else {
-      acc.reset();
-      acc.write(part + P.slot_floats, P.R, rows);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc.m[n][e] = sm[n][e];
+        acc.l[n][e] = sl[n][e];
+      }
     }
-    first.sum_rows();
-    first.write(part, P.R, rows);
-  } else {
     acc.sum_rows();
-    acc.write(part, P.R, rows);
+    acc.write(part + P.slot_floats, P.R, rows);
   }
   __syncthreads();
   const float* parts = reinterpret_cast<const float*>(smem + off_ring);
@@ -240,7 +221,7 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int path = 0; path < (PATH == kPathGated ? 2 : 1); ++path) {
-      const bool is_swa = PATH == kPathSWA || path == 1;
+      const bool is_swa = PATH == kPathSWA || (PATH == kPathGated && path == 0);
       const float* pw = parts + path * P.slot_floats;
       float m = -INFINITY;
 #pragma unroll
@@ -277,12 +258,17 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
   }
 }
 
+template <int D, int PATH, int NT>
+static cudaError_t launch_rows_of(const Params& P, unsigned grid, uint32_t smem, cudaStream_t stream) {
+  const cudaError_t ce = allow_smem<sa_paged_unit_kernel<D, PATH, NT>>(200u * 1024);
+  if (ce != cudaSuccess) return ce;
+  sa_paged_unit_kernel<D, PATH, NT><<<grid, kUnitThreads, smem, stream>>>(P);
+  return cudaGetLastError();
+}
+
 template <int D, int PATH>
 static cudaError_t launch_unit(const Params& P, unsigned grid, uint32_t smem, cudaStream_t stream) {
-  const cudaError_t ce = allow_smem<sa_paged_unit_kernel<D, PATH>>(200u * 1024);
-  if (ce != cudaSuccess) return ce;
-  sa_paged_unit_kernel<D, PATH><<<grid, kUnitThreads, smem, stream>>>(P);
-  return cudaGetLastError();
+  return P.R <= 8 ? launch_rows_of<D, PATH, 1>(P, grid, smem, stream) : launch_rows_of<D, PATH, 2>(P, grid, smem, stream);
 }
 
 }  // namespace prow
@@ -309,7 +295,7 @@ sa_status_t launch_paged_unit(const PagedProblem& pb, Path path, int row_limit, 
   P.list_keys = int(paged_unit_keys(pb, path, P.tb)) + 2 * kKeys;
   const uint32_t pitch = uint32_t(pb.d) * 2 + 16;
   auto bytes = [&](int stages) {
-    return (uint32_t(P.R) * pitch + uint32_t(P.list_keys) * 12 + 127) / 128 * 128 +
+    return (uint32_t(P.R) * pitch + uint32_t(P.list_keys) * 8 + 127) / 128 * 128 +
            uint32_t(kUnitWarps * stages) * 2 * kKeys * pitch;
   };
   // three stages where two such blocks still fit an SM
