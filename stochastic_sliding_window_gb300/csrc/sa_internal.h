@@ -165,6 +165,7 @@ struct PagedProblem {
   const float* gate_swa;
   void* out;
   int32_t* err;
+  int sa_limit;              // requests with more new tokens may go to the SA tiles (paged_sa_tiled)
 };
 
 // Row kernel (sa_paged_rows.cu).  Requests with more than row_limit new
@@ -187,9 +188,33 @@ sa_status_t launch_paged_unit(const PagedProblem& pb, Path path, int row_limit,
 // row_limit new tokens, into pb.out; with `gate` (logits [T, Hq]) as fp32
 // gated rows into part_out [T, Hq, d] instead.
 bool paged_tiles_supported(const PagedProblem& pb);
-size_t paged_tiles_workspace_bytes(const PagedProblem& pb, int sms);
+size_t paged_tiles_workspace_bytes(const PagedProblem& pb, bool sa, int sms);
 sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const float* gate,
                                float* part_out, void* workspace, int sms, cudaStream_t stream);
+int paged_tile_tokens(const PagedProblem& pb);  // tokens of a tile
+
+// The requests' tokens in sigma's order (sa_paged_order.cu), for those whose
+// SA path the tile kernel takes (paged_sa_tiled).
+struct SaOrder {
+  uint2* list;     // [requests taken][cap] tokens in sigma's order: row of the
+                   // caches at kv head 0 (0xffffffff: bad page), position
+  int32_t* place;  // the same: places in sigma
+  int4* members;   // [T] new tokens in sigma's order, a request's from q_start on:
+                   // first and last list entry of the window, row, position
+  int32_t* chunks; // [T + B] key chunks before each of a request's tiles, from q_start + b on
+  int2* info;      // [B] list number, members (0: not taken)
+  int cap;         // entries of one list
+};
+// Whether a request's SA path goes to the tile kernel: enough window keys in
+// all to be worth passing over its whole list.
+__host__ __device__ inline bool paged_sa_tiled(int n, int len, int half, int row_limit) {
+  return n > row_limit && (long long)n * (2LL * half + 1) >= len;
+}
+size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit);
+sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_tokens, void* workspace,
+                               SaOrder* order, cudaStream_t stream);
+sa_status_t launch_paged_sa_tiles(const PagedProblem& pb, const SaOrder& order, const float* gate,
+                                  const float* swa_part, void* workspace, int sms, cudaStream_t stream);
 
 // sigma^{-1} kernels.
 sa_status_t launch_inverse_perm(const int32_t* perm, int32_t* inv, int batch, int n,

@@ -394,6 +394,7 @@ static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
   pb.max_pages = p->max_pages;
   pb.window_swa = path == kPathGated && p->window_swa > 0 ? p->window_swa : p->window;
   pb.half = p->window / 2;
+  pb.sa_limit = 0x7fffffff;
   pb.perm_rows = p->perm_rows;
   pb.perm_len = p->perm_len;
   pb.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(float(pb.d));
@@ -411,16 +412,18 @@ static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
 constexpr int kRowLimit = 64;
 
 struct Choice {
-  bool tiles, rows, unit;
+  bool tiles;     // SWA (or the gated pair's SWA term) of requests beyond row_limit by tiles
+  bool sa_tiles;  // SA of such requests by tiles, where paged_sa_tiled says so
+  bool rows, unit;
   int row_limit;  // new tokens per request that the row kernel still takes
 };
 
 static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
-  Choice c{false, true, false, 0x7fffffff};
-  if (path != kPathSA && kernel != SA_PAGED_ROWS && paged_tiles_supported(pb)) {
-    if (kernel == SA_PAGED_TILES) return Choice{true, false, false, 0};
+  Choice c{false, false, true, false, 0x7fffffff};
+  if (kernel != SA_PAGED_ROWS && paged_tiles_supported(pb)) {
+    if (kernel == SA_PAGED_TILES) return Choice{true, false, false, false, 0};
     const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
-    if (pb.max_new > limit) c = Choice{true, true, false, limit};
+    if (pb.max_new > limit) c = Choice{path != kPathSA, path != kPathSWA, true, false, limit};
   }
   // few units of few keys: the unit kernel instead of the row kernel
   if (paged_unit_fits(pb, path, c.row_limit, sms)) {
@@ -433,14 +436,19 @@ static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
 static size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Workspace {
-  size_t rows, tiles, swa_part;  // parts, in this order
-  size_t total() const { return rows + tiles + swa_part; }
+  size_t rows, tiles, order, swa_part;  // parts, in this order (both tile kernels use `tiles`)
+  size_t total() const { return rows + tiles + order + swa_part; }
 };
 
 static Workspace workspace_parts(const PagedProblem& pb, Path path, const Choice& c, int sms) {
-  Workspace w{0, 0, 0};
+  Workspace w{0, 0, 0, 0};
   if (c.rows) w.rows = round256(paged_rows_workspace_bytes(pb, path, c.row_limit, sms));
-  if (c.tiles) w.tiles = round256(paged_tiles_workspace_bytes(pb, sms));
+  if (c.tiles) w.tiles = round256(paged_tiles_workspace_bytes(pb, false, sms));
+  if (c.sa_tiles) {
+    const size_t sa = round256(paged_tiles_workspace_bytes(pb, true, sms));
+    w.tiles = w.tiles > sa ? w.tiles : sa;
+    w.order = paged_order_workspace_bytes(pb, c.row_limit);
+  }
   if (c.tiles && path == kPathGated) w.swa_part = round256(size_t(pb.T) * pb.Hq * pb.d * 4);
   return w;
 }
@@ -485,9 +493,16 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   pb.out = out;
   pb.err = prm->err ? prm->err : dev.error_word;
   char* const w = static_cast<char*>(ws);
-  float* const swa_part = parts.swa_part ? reinterpret_cast<float*>(w + parts.rows + parts.tiles) : nullptr;
+  float* const swa_part = parts.swa_part ? reinterpret_cast<float*>(w + parts.rows + parts.tiles + parts.order) : nullptr;
   if (ch.tiles) {
     st = launch_paged_tiles(pb, ch.row_limit, gate_swa, swa_part, w + parts.rows, sms, stream);
+    if (st != SA_OK) return st;
+  }
+  if (ch.sa_tiles) {
+    pb.sa_limit = ch.row_limit;
+    SaOrder order;
+    st = launch_paged_order(pb, ch.row_limit, paged_tile_tokens(pb), w + parts.rows + parts.tiles, &order, stream);
+    if (st == SA_OK) st = launch_paged_sa_tiles(pb, order, gate_sa, swa_part, w + parts.rows, sms, stream);
     if (st != SA_OK) return st;
   }
   if (ch.unit) {

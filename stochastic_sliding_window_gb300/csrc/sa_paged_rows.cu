@@ -585,6 +585,7 @@ void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, 
   P.T = pb.T;
   P.max_new = pb.max_new;
   P.row_limit = row_limit;
+  P.sa_limit = pb.sa_limit;
   P.Hq = pb.Hq;
   P.Hkv = pb.Hkv;
   P.g = pb.g;

@@ -37,7 +37,7 @@ struct Params {
   float* part;            // partial slots, then Desc[workers]; nullptr: never split
   Desc* desc;
   long long q_stride, perm_stride;
-  int B, T, max_new, row_limit, Hq, Hkv, g, page, page_shift, num_pages, max_pages;
+  int B, T, max_new, row_limit, sa_limit, Hq, Hkv, g, page, page_shift, num_pages, max_pages;
   int page_rows;          // rows of D elements between pages
   int w, half, perm_len;
   int tb, rg, R;          // tokens and rows of a unit; row groups of a kv head (g > 16)
@@ -88,6 +88,7 @@ __device__ __forceinline__ Request load_request(const Params& P, int b, bool rep
     if (report && q1 != r.q0) atomicOr(P.err, SA_ERRBIT_RANGE);
     r.n = 0;
   }
+  if (PATH != kPathSWA && paged_sa_tiled(r.n, r.len, P.half, P.sa_limit)) r.n = 0;
   const bool swa_here = r.n <= P.row_limit;
   if (PATH == kPathSWA && !swa_here) r.n = 0;
   if (PATH != kPathSWA) r.tsa = int((min(2LL * P.half + 1, (long long)P.perm_len) + kKeys - 1) / kKeys);

@@ -1,6 +1,7 @@
-// Tile kernel of the paged-cache attention: SWA (any window, full causal
-// among them) for requests that bring many new tokens, on the 5th-generation
-// tensor cores.
+// Tile kernel of the paged-cache attention for requests that bring many new
+// tokens, on the 5th-generation tensor cores: SWA (any window, full causal
+// among them), and SA over the order that sa_paged_order.cu makes of a
+// request's tokens.
 //
 // Mathematics.  A tile is up to 256 query rows that share a kv head -- the g
 // query heads of Bt = floor(256 / g) consecutive new tokens, row r = t g + j
@@ -17,6 +18,14 @@
 // softmax of a half (128 rows x 128 keys) must take no longer than the other
 // half's two MMAs: one thread per row holds the row's 128 scores in
 // registers, one pass, masks only in the chunks that a window's end crosses.
+//
+// SA.  In sigma's order -- the request's tokens listed by their place in sigma,
+// those that do not exist yet left out -- every row's window is a run of
+// consecutive entries, and the new tokens (members) that follow each other in
+// the list share most of theirs.  So a tile is Bt members that follow each
+// other, its keys the list from the first one's window to the last one's, and
+// the rest is as for SWA, but for the causal rule among the new tokens
+// themselves (older keys precede every row) and rows that TMA cannot box.
 //
 // Split.  One block per SM.  All chunks of all tiles, laid end to end
 // (request, kv head, tile, chunk), are cut into equal runs, one per block, so
@@ -77,6 +86,13 @@ struct Params {
   uint32_t off_k, off_v, off_bad, off_seg, off_bar;
   float scale_log2;
   long long timeout_cycles;
+  // SA: what sa_paged_order.cu made of sigma, and the rows that it numbers
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long q_stride;
+  SaOrder order;
+  const float* swa_part;  // fp32 [T, Hq, D], added to the rows; nullptr: none
 };
 
 // Barriers (8 bytes each).  A phase is one use; chunks and tiles are counted
@@ -168,14 +184,22 @@ __device__ __forceinline__ long long floor_sum(long long n, long long m, long lo
   return s;
 }
 
+// SA: n counts the request's members (its new tokens in sigma's order) and its
+// keys are entries of the list of its tokens in that order.
 struct Request {
-  int q0, n, len;
+  int q0, n, len, b;
 };
+template <bool SA>
 __device__ __forceinline__ Request load_request(const Params& P, int b, bool report) {
   Request r;
+  r.b = b;
   r.q0 = P.q_start[b];
   const int q1 = P.q_start[b + 1];
   r.len = P.seq_lens[b];
+  if (SA) {  // (checked where the order was made; 0 members where it was not)
+    r.n = P.order.info[b].y;
+    return r;
+  }
   r.n = q1 - r.q0;
   const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= P.T && r.n <= P.max_new && r.n <= r.len &&
                   (long long)r.len <= (long long)P.max_pages * P.page;
@@ -187,26 +211,36 @@ __device__ __forceinline__ Request load_request(const Params& P, int b, bool rep
   return r;
 }
 
-// First key and number of keys of tile `grp` of a request.
+// First key and the key after the last of tile `grp` of a request.
+template <bool SA>
 __device__ __forceinline__ int tile_lo(const Params& P, const Request& r, int grp) {
+  if (SA) return P.order.members[r.q0 + grp * P.Bt].x;
   return max(0, r.len - r.n + grp * P.Bt - P.w + 1);
 }
+template <bool SA>
 __device__ __forceinline__ int tile_hi(const Params& P, const Request& r, int grp) {
+  if (SA) return P.order.members[r.q0 + min(r.n, (grp + 1) * P.Bt) - 1].y + 1;
   return r.len - r.n + min(r.n, (grp + 1) * P.Bt);
-}
-__device__ __forceinline__ int tile_chunks(const Params& P, const Request& r, int grp) {
-  return (tile_hi(P, r, grp) - tile_lo(P, r, grp) + kKC - 1) / kKC;
 }
 __device__ __forceinline__ int num_tiles(const Params& P, const Request& r) {
   return (r.n + P.Bt - 1) / P.Bt;
 }
 // Chunks of the request's first `k` tiles (of one kv head).
+template <bool SA>
+__device__ __forceinline__ long long chunks_before(const Params& P, const Request& r, int k);
+template <bool SA>
+__device__ __forceinline__ int tile_chunks(const Params& P, const Request& r, int grp) {
+  if (SA) return int(chunks_before<SA>(P, r, grp + 1) - chunks_before<SA>(P, r, grp));
+  return (tile_hi<SA>(P, r, grp) - tile_lo<SA>(P, r, grp) + kKC - 1) / kKC;
+}
+template <bool SA>
 __device__ __forceinline__ long long chunks_before(const Params& P, const Request& r, int k) {
+  if (SA) return P.order.chunks[r.q0 + r.b + k];
   const int nt = num_tiles(P, r);
   long long s = 0;
   if (k == nt && k > 0) {  // the last tile may be short
     --k;
-    s = tile_chunks(P, r, k);
+    s = tile_chunks<SA>(P, r, k);
   }
   // tiles whose window reaches the first key: hi = c + (i + 1) Bt keys
   const long long c = r.len - r.n;
@@ -237,7 +271,8 @@ struct Seg {
 // the S MMAs of the third tile after it are done, which follow every softmax
 // warp's read of the second's.
 struct Shared {
-  int t0, nt, pos0, lo;  // first token's row, tokens, first position, first key
+  int t0, nt, pos0, lo;  // first token's row, tokens, first position, first key (SA:
+                         // t0 is the first member's index, pos0 unused)
   int kvh, c0, c1, nch;
   int more;              // another tile part follows
   int join;              // last block that holds a part of a tile cut here
@@ -250,6 +285,7 @@ struct Cursor {
   int b, kvh, grp, off, cut, nt;
   bool done;
 };
+template <bool SA>
 __device__ __forceinline__ Cursor make_cursor(const Params& P, const Start& s) {
   Cursor c;
   c.pos = s.begin;
@@ -262,11 +298,12 @@ __device__ __forceinline__ Cursor make_cursor(const Params& P, const Start& s) {
   c.done = s.begin >= s.end;
   c.nt = 0;
   if (!c.done) {
-    c.r = load_request(P, c.b, false);
+    c.r = load_request<SA>(P, c.b, false);
     c.nt = num_tiles(P, c.r);
   }
   return c;
 }
+template <bool SA>
 __device__ __forceinline__ void next_tile(const Params& P, Cursor& c) {
   c.off = 0;
   if (++c.grp < c.nt) return;
@@ -278,16 +315,17 @@ __device__ __forceinline__ void next_tile(const Params& P, Cursor& c) {
       c.done = true;
       return;
     }
-    c.r = load_request(P, c.b, false);
+    c.r = load_request<SA>(P, c.b, false);
   } while (c.r.n == 0);
   c.nt = num_tiles(P, c.r);
 }
 // The next tile part of the run; false at its end.
+template <bool SA>
 __device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
   if (c.done) return false;
   if (!c.cut && c.off != 0) {  // the tile cut here is the previous block's
-    c.pos += tile_chunks(P, c.r, c.grp) - c.off;
-    next_tile(P, c);
+    c.pos += tile_chunks<SA>(P, c.r, c.grp) - c.off;
+    next_tile<SA>(P, c);
     if (c.done) return false;
   }
   if (c.pos >= c.end) return false;
@@ -295,13 +333,13 @@ __device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
   s.b = c.b;
   s.kvh = c.kvh;
   s.grp = c.grp;
-  s.nch = tile_chunks(P, c.r, c.grp);
+  s.nch = tile_chunks<SA>(P, c.r, c.grp);
   s.c0 = c.off;
   s.c1 = c.cut ? int(min((long long)s.nch, c.off + (c.end - c.pos))) : s.nch;
   s.pos = c.pos;
   c.pos += s.c1 - s.c0;
   if (s.c1 == s.nch) {
-    next_tile(P, c);
+    next_tile<SA>(P, c);
   } else {
     c.done = true;  // the run ends inside this tile
   }
@@ -309,15 +347,16 @@ __device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
 }
 
 // Warp 0: this block's run (collective over its lanes).
+template <bool SA>
 __device__ Start find_start(const Params& P) {
   const int lane = threadIdx.x & 31;
   long long total = 0, tiles = 0;
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     if (b0 + lane < P.B) {
-      const Request r = load_request(P, b0 + lane, blockIdx.x == 0);
+      const Request r = load_request<SA>(P, b0 + lane, blockIdx.x == 0);
       if (r.n > 0) {
         const int nt = num_tiles(P, r);
-        total += P.Hkv * chunks_before(P, r, nt);
+        total += P.Hkv * chunks_before<SA>(P, r, nt);
         tiles += (long long)P.Hkv * nt;
       }
     }
@@ -342,8 +381,8 @@ __device__ Start find_start(const Params& P) {
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     long long x = 0;
     if (b0 + lane < P.B) {
-      const Request r = load_request(P, b0 + lane, false);
-      if (r.n > 0) x = P.Hkv * chunks_before(P, r, num_tiles(P, r));
+      const Request r = load_request<SA>(P, b0 + lane, false);
+      if (r.n > 0) x = P.Hkv * chunks_before<SA>(P, r, num_tiles(P, r));
     }
     long long sum = x;
 #pragma unroll
@@ -356,18 +395,18 @@ __device__ Start find_start(const Params& P) {
       const int src = __ffs(hit) - 1;
       s.b = b0 + src;
       long long rel = s.begin - (before + __shfl_sync(0xffffffffu, sum - x, src));
-      const Request r = load_request(P, s.b, false);
+      const Request r = load_request<SA>(P, s.b, false);
       const int nt = num_tiles(P, r);
-      const long long per_head = chunks_before(P, r, nt);
+      const long long per_head = chunks_before<SA>(P, r, nt);
       s.kvh = int(rel / per_head);
       rel -= s.kvh * per_head;
       int lo = 0, hi = nt - 1;  // the last tile that starts at or before rel
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (chunks_before(P, r, mid) <= rel) lo = mid; else hi = mid - 1;
+        if (chunks_before<SA>(P, r, mid) <= rel) lo = mid; else hi = mid - 1;
       }
       s.grp = lo;
-      s.tile_off = rel - chunks_before(P, r, lo);
+      s.tile_off = rel - chunks_before<SA>(P, r, lo);
       break;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
@@ -387,6 +426,14 @@ struct Keys {
   int steps;        // 16-key steps that hold keys
   int pad[2];
 };
+struct SaKeys : Keys {
+  uint32_t fresh[4];  // bit j: key j is one of the request's new tokens
+  int toks[kKC];
+};
+template <bool SA>
+struct KeysOf { using T = Keys; };
+template <>
+struct KeysOf<true> { using T = SaKeys; };
 
 // A run of `len` rows of a page from row `in` to rows r .. of a stage, in
 // boxes of 64, 16, 4 and 1 rows; or `len` copies of one row.
@@ -417,16 +464,16 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
     const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
     return __all_sync(0xffffffffu, ok);
   };
-  Cursor cur = make_cursor(P, start);
+  Cursor cur = make_cursor<false>(P, start);
   Seg s, ahead;
   int n = 0, x = 0;             // chunks and tiles so far
   int nq = 0, nk = 0, nv = 0;   // Q, K and V loads begun
   bool ok = true;
-  bool more = next_seg(P, cur, ahead);
+  bool more = next_seg<false>(P, cur, ahead);
   for (; ok && more; ++x) {
     s = ahead;
-    more = next_seg(P, cur, ahead);
-    const int lo = tile_lo(P, s.r, s.grp), hi = tile_hi(P, s.r, s.grp);
+    more = next_seg<false>(P, cur, ahead);
+    const int lo = tile_lo<false>(P, s.r, s.grp), hi = tile_hi<false>(P, s.r, s.grp);
     const int i0 = s.grp * P.Bt;
     const int32_t* table = P.table + (long long)s.b * P.max_pages;
     // page of table column `col` (columns hi and on: not looked at)
@@ -557,9 +604,126 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
   __syncwarp();
 }
 
-// ------------------------------------------------------------------ MMA issue
+// SA: rows from anywhere, so cp.async by three warps (96 threads).  The list's
+// entries of a chunk are read one chunk ahead, by one or two keys a thread.
+constexpr int kSaProducers = 96;
+
 template <int D, int NS>
-__device__ void mma_role(const Params& P, bool more, const Shared* seg, const Keys* keys,
+__device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
+                                 uint32_t bars, volatile int* abort_flag, volatile int* vote) {
+  using BR = Bars<NS>;
+  constexpr uint32_t kTile = kKC * D * 2;
+  constexpr int CPR = D / 8;               // 16-byte chunks per row
+  constexpr int RPP = kSaProducers / CPR;  // rows per pass
+  const int lane = threadIdx.x & 31;
+  const int tid = threadIdx.x < 32 ? int(threadIdx.x) : int(threadIdx.x) - 32;  // warps 0, 2, 3
+  const int cc = tid % CPR, r_first = tid / CPR;
+  const uint32_t col = uint32_t(cc >> 3) * (kKC * 128), c8 = uint32_t(cc & 7);
+  uint32_t* srow = reinterpret_cast<uint32_t*>(smem + P.off_seg + 4 * sizeof(Shared));  // [2][128]
+  int step = 0;
+  // every producer learns whether thread 0's wait succeeded; also orders
+  // their shared-memory writes before what follows
+  auto agree = [&](uint32_t bar, uint32_t parity, bool need) {
+    if (tid == 0)
+      vote[step & 1] = !need || bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag) ? 1 : 0;
+    asm volatile("bar.sync 1, %0;" ::"n"(kSaProducers) : "memory");
+    const bool ok = vote[step & 1] != 0;
+    ++step;
+    return ok;
+  };
+  const char* kbase = reinterpret_cast<const char*>(P.k) + cc * 16;
+  const char* vbase = reinterpret_cast<const char*>(P.v) + cc * 16;
+  auto rows_in = [&](const char* base, uint32_t dst, const uint32_t* rows) {
+#pragma unroll 6
+    for (int i = r_first; i < kKC; i += RPP) {
+      const uint32_t r = rows[i];
+      const uint32_t to = dst + uint32_t(i) * 128 + ((c8 ^ uint32_t(i & 7)) << 4);
+      const int bytes = r != 0xffffffffu ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                   "l"(base + uint64_t(bytes ? r : 0u) * (D * 2)), "r"(bytes)
+                   : "memory");
+    }
+  };
+  Cursor cur = make_cursor<true>(P, start);
+  Seg s, ahead;
+  int n = 0, x = 0;
+  bool ok = true;
+  bool more = next_seg<true>(P, cur, ahead);
+  for (; ok && more; ++x) {
+    s = ahead;
+    more = next_seg<true>(P, cur, ahead);
+    const int lo = tile_lo<true>(P, s.r, s.grp), hi = tile_hi<true>(P, s.r, s.grp);
+    const int m0 = s.r.q0 + s.grp * P.Bt, nt = min(P.Bt, s.r.n - s.grp * P.Bt);
+    const uint2* list = P.order.list + (long long)P.order.info[s.b].x * P.order.cap;
+    const int first_new = s.r.len - (P.q_start[s.b + 1] - s.r.q0);
+    auto entry = [&](int c, int at) {
+      const int j = lo + c * kKC + at;
+      return j < hi ? list[j] : make_uint2(0xffffffffu, 0x7fffffffu);
+    };
+    const bool two = tid < kKC - kSaProducers;
+    uint2 e0 = entry(s.c0, tid), e1 = two ? entry(s.c0, kSaProducers + tid) : make_uint2(0u, 0u);
+    if (!(ok = agree(BR::kQfree, uint32_t(x - 1), x > 0))) break;
+    if (tid == 0) {
+      Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
+      sh->t0 = m0;
+      sh->nt = nt;
+      sh->pos0 = 0;
+      sh->lo = lo;
+      sh->kvh = s.kvh;
+      sh->c0 = s.c0;
+      sh->c1 = s.c1;
+      sh->nch = s.nch;
+      sh->more = more;
+      sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
+      mbar_arrive(bars + 8 * BR::kQfull);
+    }
+    for (int r = r_first; r < nt * P.g; r += RPP) {
+      const int t = r / P.g, j = r - t * P.g;
+      const int row = P.order.members[m0 + t].z;
+      cp_async16(sbase + uint32_t(cc >> 3) * (kRows * 128) + uint32_t(r) * 128 + ((c8 ^ uint32_t(r & 7)) << 4),
+                 P.q + (long long)row * P.q_stride + (s.kvh * P.g + j) * D + cc * 8);
+    }
+    cp_async_arrive_noinc(bars + 8 * BR::kQfull);
+    for (int c = s.c0; c < s.c1; ++c, ++n) {
+      const int st = n % NS;
+      SaKeys* keys = reinterpret_cast<SaKeys*>(smem + P.off_bad) + (n % kKeySlots);
+      uint32_t* rows = srow + (n & 1) * kKC;
+      auto put = [&](int at, uint2 e) {
+        const int j = lo + c * kKC + at;
+        const uint32_t bad = __ballot_sync(0xffffffffu, j < hi && e.x == 0xffffffffu);
+        const uint32_t fresh = __ballot_sync(0xffffffffu, j < hi && int(e.y) >= first_new);
+        rows[at] = e.x == 0xffffffffu ? e.x : e.x + uint32_t(s.kvh);
+        keys->toks[at] = int(e.y);
+        if (lane == 0) {
+          keys->bad[at >> 5] = bad;
+          keys->fresh[at >> 5] = fresh;
+        }
+      };
+      put(tid, e0);
+      if (two) put(kSaProducers + tid, e1);
+      if (tid == 0) {
+        keys->good = 1;  // rows that are not there are zeros
+        keys->steps = kKC / 16;
+      }
+      if (c + 1 < s.c1) {
+        e0 = entry(c + 1, tid);
+        if (two) e1 = entry(c + 1, kSaProducers + tid);
+      }
+      if (!(ok = agree(BR::kKfree + st, uint32_t(n / NS - 1), n >= NS))) break;
+      rows_in(kbase, sbase + P.off_k + uint32_t(st) * kTile + col, rows);
+      cp_async_arrive_noinc(bars + 8 * (BR::kKfull + st));
+      if (tid == 0) mbar_arrive(bars + 8 * (BR::kKfull + st));  // the key words
+      if (!(ok = agree(BR::kVfree + st, uint32_t(n / NS - 1), n >= NS))) break;
+      rows_in(vbase, sbase + P.off_v + uint32_t(st) * kTile + col, rows);
+      cp_async_arrive_noinc(bars + 8 * (BR::kVfull + st));
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // own copies land before exit
+}
+
+// ------------------------------------------------------------------ MMA issue
+template <int D, int NS, bool SA>
+__device__ void mma_role(const Params& P, bool more, const Shared* seg, const typename KeysOf<SA>::T* keys,
                          uint32_t sbase, uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
@@ -578,6 +742,7 @@ __device__ void mma_role(const Params& P, bool more, const Shared* seg, const Ke
     if (!wait(BR::kPfull + h, uint32_t(n))) return false;
     if (h == 0 && !wait(BR::kVfull + n % NS, uint32_t(n / NS))) return false;
     if (first && x > 0 && !wait(BR::kOfree + h, uint32_t(x - 1))) return false;
+    if (SA) fence_proxy_async_smem();  // cp.async (generic proxy) data -> tensor core reads
     tc_fence_after();
     const uint32_t o = tmem + uint32_t(2 * kKC + h * D), p = tmem + uint32_t(h * kKC);
     const uint64_t b = vd + uint64_t(n % NS) * (kTile / 16);
@@ -594,6 +759,7 @@ __device__ void mma_role(const Params& P, bool more, const Shared* seg, const Ke
     return true;
   };
   auto qk = [&](int h, int n, bool last) {
+    if (SA) fence_proxy_async_smem();
     tc_fence_after();
     const uint32_t d = tmem + uint32_t(h * kKC);
     const uint64_t b0 = kd + uint64_t(n % NS) * (kTile / 16);
@@ -638,8 +804,8 @@ __device__ void mma_role(const Params& P, bool more, const Shared* seg, const Ke
 }
 
 // ------------------------------------------------------------------ softmax
-template <int D, int NS>
-__device__ void softmax_role(const Params& P, bool more, const Shared* seg, const Keys* keys,
+template <int D, int NS, bool SA>
+__device__ void softmax_role(const Params& P, bool more, const Shared* seg, const typename KeysOf<SA>::T* keys,
                              uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -663,13 +829,15 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
     more = sh->more != 0;
     const int c0 = sh->c0, c1 = sh->c1;
     const bool live = t < sh->nt;
-    const int pos = sh->pos0 + t;
+    int4 mem = make_int4(0, -1, 0, 0);
+    if (SA && live) mem = P.order.members[sh->t0 + t];
+    const int pos = SA ? mem.w : sh->pos0 + t;
     // the row's keys as columns of chunk 0
-    const int khi = live ? pos - sh->lo : -1;
-    const int klo = max(0, pos - P.w + 1) - sh->lo;
+    const int khi = live ? (SA ? mem.y : pos) - sh->lo : -1;
+    const int klo = (SA ? mem.x : max(0, pos - P.w + 1)) - sh->lo;
     const bool whole = c0 == 0 && c1 == sh->nch;
     const int slot = int(blockIdx.x) * 2 + (c0 == 0 ? 1 : 0);
-    const size_t orow = live ? size_t(sh->t0 + t) * P.Hq + size_t(sh->kvh) * P.g + j : 0;
+    const size_t orow = live ? size_t(SA ? mem.z : sh->t0 + t) * P.Hq + size_t(sh->kvh) * P.g + j : 0;
     if (sh->join >= 0 && h == 0 && quad == 0 && lane == 0) {
       Desc d;
       d.valid = 1;
@@ -689,7 +857,12 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
       for (int q = 0; q < 4; ++q) tmem_ld32_async(sb + q * 32, v[q]);
       const uint4 bad = *reinterpret_cast<const uint4*>(keys[n % kKeySlots].bad);
       const int lo = klo - c * kKC, hi = khi - c * kKC;
-      const bool clear = lo <= 0 && hi >= kKC - 1 && (bad.x | bad.y | bad.z | bad.w) == 0u;
+      bool clear = lo <= 0 && hi >= kKC - 1 && (bad.x | bad.y | bad.z | bad.w) == 0u;
+      uint4 fresh = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (SA) {
+        fresh = *reinterpret_cast<const uint4*>(keys[n % kKeySlots].fresh);
+        clear = clear && (fresh.x | fresh.y | fresh.z | fresh.w) == 0u;
+      }
       tmem_wait_ld();
 #pragma unroll
       for (int q = 0; q < 4; ++q) reg_fence(v[q]);
@@ -697,7 +870,14 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
         const uint32_t bw[4] = {bad.x, bad.y, bad.z, bad.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint32_t keep = band_bits(lo, hi, q * 32) & ~bw[q];
+          uint32_t keep = band_bits(lo, hi, q * 32) & ~bw[q];
+          if constexpr (SA) {  // of the new tokens, the later ones are left out
+            const uint32_t fw[4] = {fresh.x, fresh.y, fresh.z, fresh.w};
+            for (uint32_t f = fw[q]; f != 0u; f &= f - 1u) {
+              const int e = __ffs(int(f)) - 1;
+              if (keys[n % kKeySlots].toks[q * 32 + e] > pos) keep &= ~(1u << e);
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((keep >> e) & 1u)) v[q][e] = __float_as_uint(-INFINITY);
@@ -799,7 +979,18 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
           o[2 * e] = __float_as_uint(y.x);
           o[2 * e + 1] = __float_as_uint(y.y);
         }
-        if (P.gate != nullptr) {
+        if (SA && P.swa_part != nullptr) {
+          const float4* add = reinterpret_cast<const float4*>(P.swa_part + orow * D + q * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 y = add[e];
+            o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + y.x);
+            o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + y.y);
+            o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + y.z);
+            o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + y.w);
+          }
+        }
+        if (!SA && P.gate != nullptr) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[8];
@@ -826,12 +1017,13 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
   }
 }
 
-template <int D, int NS>
+template <int D, int NS, bool SA>
 __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __grid_constant__ Params P) {
   using BR = Bars<NS>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Start s_start;
   __shared__ bool s_any;
+  __shared__ int s_vote[2];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + P.off_bar;
@@ -839,21 +1031,22 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 4);
   const int warp = threadIdx.x >> 5;
   if (warp == 0) {
-    const Start s = find_start(P);
-    Cursor cur = make_cursor(P, s);
+    const Start s = find_start<SA>(P);
+    Cursor cur = make_cursor<SA>(P, s);
     Seg seg;
-    const bool any = next_seg(P, cur, seg);
+    const bool any = next_seg<SA>(P, cur, seg);
     if (threadIdx.x == 0) {
       s_start = s;
       s_any = any;
     }
   } else if (threadIdx.x == 64) {
-    mbar_init(bars + 8 * BR::kQfull, 1);
+    // SA: the producers' copies, and thread 0 for what it and they wrote besides
+    mbar_init(bars + 8 * BR::kQfull, SA ? kSaProducers + 1 : 1);
     mbar_init(bars + 8 * BR::kQfree, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bars + 8 * (BR::kKfull + i), 1);
+      mbar_init(bars + 8 * (BR::kKfull + i), SA ? kSaProducers + 1 : 1);
       mbar_init(bars + 8 * (BR::kKfree + i), 1);
-      mbar_init(bars + 8 * (BR::kVfull + i), 1);
+      mbar_init(bars + 8 * (BR::kVfull + i), SA ? kSaProducers : 1);
       mbar_init(bars + 8 * (BR::kVfree + i), 1);
     }
     for (int h = 0; h < 2; ++h) {
@@ -879,15 +1072,17 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   const uint32_t tmem = *tmem_slot;
   const bool any = s_any;
   const Shared* seg = reinterpret_cast<const Shared*>(smem + P.off_seg);
-  const Keys* keys = reinterpret_cast<const Keys*>(smem + P.off_bad);
+  const auto* keys = reinterpret_cast<const typename KeysOf<SA>::T*>(smem + P.off_bad);
 
   if (warp >= kFirstSoftmaxWarp) {
-    softmax_role<D, NS>(P, any, seg, keys, tmem, bars, abort_flag);
+    softmax_role<D, NS, SA>(P, any, seg, keys, tmem, bars, abort_flag);
+  } else if (warp == kMmaWarp) {
+    if ((threadIdx.x & 31) == 0) mma_role<D, NS, SA>(P, any, seg, keys, sbase, tmem, bars, abort_flag);
+    __syncwarp();
+  } else if (SA) {
+    sa_producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, s_vote);
   } else if (warp == 0) {
     producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag);
-  } else if (warp == kMmaWarp) {
-    if ((threadIdx.x & 31) == 0) mma_role<D, NS>(P, any, seg, keys, sbase, tmem, bars, abort_flag);
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -900,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
 
 // Joins the parts of each tile that the runs cut, in block order.  Block
 // (c, y) takes columns of the tile that starts in run c.
-template <int D>
+template <int D, bool SA>
 __global__ void __launch_bounds__(kRows) sa_paged_tiles_join_kernel(const __grid_constant__ Params P) {
   const int c0 = blockIdx.x;
   const Desc d = P.desc[c0];
@@ -930,21 +1125,36 @@ __global__ void __launch_bounds__(kRows) sa_paged_tiles_join_kernel(const __grid
     }
   }
   const int t = row / P.g, j = row - t * P.g;
-  const size_t orow = size_t(d.t0 + t) * P.Hq + size_t(d.kvh) * P.g + j;
+  const int trow = SA ? P.order.members[d.t0 + t].z : d.t0 + t;
+  const size_t orow = size_t(trow) * P.Hq + size_t(d.kvh) * P.g + j;
   float s = l == 0.f ? 0.f : 1.f / l;
   if (P.gate != nullptr) s *= 1.f / (1.f + expf(-P.gate[orow]));
   const int col = blockIdx.y * 16;
-  if (P.gate != nullptr) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    a[e].x *= s;
+    a[e].y *= s;
+    a[e].z *= s;
+    a[e].w *= s;
+    if (SA && P.swa_part != nullptr) {
+      const float4 y = *reinterpret_cast<const float4*>(P.swa_part + orow * D + col + 4 * e);
+      a[e].x += y.x;
+      a[e].y += y.y;
+      a[e].z += y.z;
+      a[e].w += y.w;
+    }
+  }
+  if (!SA && P.gate != nullptr) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<float4*>(P.part_out + orow * D + col + 4 * e) =
-          make_float4(a[e].x * s, a[e].y * s, a[e].z * s, a[e].w * s);
+          a[e];
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[2 * e] = pack_bf16x2(a[e].x * s, a[e].y * s);
-      w[2 * e + 1] = pack_bf16x2(a[e].z * s, a[e].w * s);
+      w[2 * e] = pack_bf16x2(a[e].x, a[e].y);
+      w[2 * e + 1] = pack_bf16x2(a[e].z, a[e].w);
     }
     st_global_2v4(P.out + orow * D + col, w);
   }
@@ -952,27 +1162,29 @@ __global__ void __launch_bounds__(kRows) sa_paged_tiles_join_kernel(const __grid
 
 // ------------------------------------------------------------------ host
 
-static bool may_cut(const PagedProblem& pb) {
-  const long long keys = min((long long)pb.window_swa + kRows, (long long)pb.max_pages * pb.page);
+static bool may_cut(const PagedProblem& pb, bool sa) {
+  const long long longest = (long long)pb.max_pages * pb.page;
+  const long long keys = sa ? longest : min((long long)pb.window_swa + kRows, longest);
   return keys >= (long long)kCutChunks * kKC;
 }
 
-template <int D, int NS>
+template <int D, int NS, bool SA>
 static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
+  using K = typename KeysOf<SA>::T;
   const uint32_t tile = kKC * D * 2;
   P.off_k = 2 * kBM * D * 2;
   P.off_v = P.off_k + NS * tile;
   P.off_bad = P.off_v + NS * tile;
-  P.off_seg = P.off_bad + kKeySlots * uint32_t(sizeof(Keys));
-  P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared));
+  P.off_seg = P.off_bad + kKeySlots * uint32_t(sizeof(K));
+  P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared)) + (SA ? 2 * kKC * 4 : 0);
   const uint32_t smem = P.off_bar + 8 * Bars<NS>::kNum + 16 + 1024;
-  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(Keys) + 4 * sizeof(Shared) + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
+  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(K) + 4 * sizeof(Shared) + 2 * kKC * 4 + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
                     kMaxSmem, "shared memory");
-  cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS>>(smem);
+  cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS, SA>>(smem);
   if (ce != cudaSuccess) return ce;
-  sa_paged_tiles_kernel<D, NS><<<sms, kThreads, smem, stream>>>(P);
+  sa_paged_tiles_kernel<D, NS, SA><<<sms, kThreads, smem, stream>>>(P);
   if ((ce = cudaGetLastError()) != cudaSuccess || P.desc == nullptr) return ce;
-  sa_paged_tiles_join_kernel<D><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
+  sa_paged_tiles_join_kernel<D, SA><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -982,17 +1194,51 @@ bool paged_tiles_supported(const PagedProblem& pb) {
   return pb.g <= ptile::kRows / 4;  // at least four tokens to a tile
 }
 
-size_t paged_tiles_workspace_bytes(const PagedProblem& pb, int sms) {
-  if (!ptile::may_cut(pb)) return 0;
+size_t paged_tiles_workspace_bytes(const PagedProblem& pb, bool sa, int sms) {
+  if (!ptile::may_cut(pb, sa)) return 0;
   const size_t part = size_t(sms) * 2 * ptile::kRows * (pb.d + 2) * 4;
   return (part + 255) / 256 * 256 + (size_t(sms) * sizeof(ptile::Desc) + 255) / 256 * 256;
 }
+
+namespace ptile {
+static void common_params(Params* P, const PagedProblem& pb, bool sa, int row_limit, void* workspace, int sms) {
+  std::memset(P, 0, sizeof(*P));
+  P->table = pb.table;
+  P->q_start = pb.q_start;
+  P->seq_lens = pb.seq_lens;
+  P->out = static_cast<__nv_bfloat16*>(pb.out);
+  if (may_cut(pb, sa)) {
+    const size_t part = size_t(sms) * 2 * kRows * (pb.d + 2) * 4;
+    P->part = static_cast<float*>(workspace);
+    P->desc = reinterpret_cast<Desc*>(static_cast<char*>(workspace) + (part + 255) / 256 * 256);
+  }
+  P->err = pb.err;
+  P->B = pb.B;
+  P->T = pb.T;
+  P->max_new = pb.max_new;
+  P->row_limit = row_limit;
+  P->Hq = pb.Hq;
+  P->Hkv = pb.Hkv;
+  P->g = pb.g;
+  P->Bt = paged_tile_tokens(pb);
+  P->page = pb.page;
+  P->num_pages = pb.num_pages;
+  P->max_pages = pb.max_pages;
+  P->w = pb.window_swa;
+  P->scale_log2 = pb.scale * 1.4426950408889634f;
+  P->timeout_cycles = wait_limit_cycles();
+}
+}  // namespace ptile
+
+int paged_tile_tokens(const PagedProblem& pb) { return ptile::kRows / pb.g; }
 
 sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const float* gate,
                                float* part_out, void* workspace, int sms, cudaStream_t stream) {
   using namespace ptile;
   Params P;
-  std::memset(&P, 0, sizeof(P));
+  common_params(&P, pb, false, row_limit, workspace, sms);
+  P.gate = gate;
+  P.part_out = part_out;
   const uint64_t d2 = uint64_t(pb.d) * 2;
   const uint64_t qdims[3] = {uint64_t(pb.d), uint64_t(pb.Hq), uint64_t(pb.T)};
   const uint64_t qst[2] = {d2, uint64_t(pb.q_stride) * 2};
@@ -1005,34 +1251,27 @@ sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const floa
     maps = encode_box_map(&P.tk[i], pb.k, 4, dims, st, box) && encode_box_map(&P.tv[i], pb.v, 4, dims, st, box);
   }
   if (!maps) return fail(SA_ERR_CUDA, "paged tile kernel: cannot encode the tensor maps");
-  P.table = pb.table;
-  P.q_start = pb.q_start;
-  P.seq_lens = pb.seq_lens;
-  P.gate = gate;
-  P.out = static_cast<__nv_bfloat16*>(pb.out);
-  P.part_out = part_out;
-  if (may_cut(pb)) {
-    const size_t part = size_t(sms) * 2 * kRows * (pb.d + 2) * 4;
-    P.part = static_cast<float*>(workspace);
-    P.desc = reinterpret_cast<Desc*>(static_cast<char*>(workspace) + (part + 255) / 256 * 256);
-  }
-  P.err = pb.err;
-  P.B = pb.B;
-  P.T = pb.T;
-  P.max_new = pb.max_new;
-  P.row_limit = row_limit;
-  P.Hq = pb.Hq;
-  P.Hkv = pb.Hkv;
-  P.g = pb.g;
-  P.Bt = kRows / pb.g;
-  P.page = pb.page;
-  P.num_pages = pb.num_pages;
-  P.max_pages = pb.max_pages;
-  P.w = pb.window_swa;
-  P.scale_log2 = pb.scale * 1.4426950408889634f;
-  P.timeout_cycles = wait_limit_cycles();
-  const cudaError_t ce = pb.d == 128 ? launch_one<128, 2>(P, sms, stream) : launch_one<64, 4>(P, sms, stream);
+  const cudaError_t ce =
+      pb.d == 128 ? launch_one<128, 2, false>(P, sms, stream) : launch_one<64, 4, false>(P, sms, stream);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged tile kernel launch: %s", cudaGetErrorString(ce));
+  return SA_OK;
+}
+
+sa_status_t launch_paged_sa_tiles(const PagedProblem& pb, const SaOrder& order, const float* gate,
+                                  const float* swa_part, void* workspace, int sms, cudaStream_t stream) {
+  using namespace ptile;
+  Params P;
+  common_params(&P, pb, true, 0, workspace, sms);
+  P.gate = gate;
+  P.swa_part = swa_part;
+  P.q = static_cast<const __nv_bfloat16*>(pb.q);
+  P.k = static_cast<const __nv_bfloat16*>(pb.k);
+  P.v = static_cast<const __nv_bfloat16*>(pb.v);
+  P.q_stride = pb.q_stride;
+  P.order = order;
+  const cudaError_t ce =
+      pb.d == 128 ? launch_one<128, 2, true>(P, sms, stream) : launch_one<64, 4, true>(P, sms, stream);
+  if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged SA tile kernel launch: %s", cudaGetErrorString(ce));
   return SA_OK;
 }
 

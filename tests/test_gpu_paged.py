@@ -79,6 +79,78 @@ def test_auto_mixes_both_kernels(path, shape):
     assert (out[b.t:] == 2.0).all()
 
 
+SA_TILE_SHAPES = {
+    "one_request": ([300], [700], 8, 2, 128, 16, 700),
+    "mha": ([300, 257, 20], [300, 1000, 21], 2, 2, 64, 7, 1500),
+    "g5": ([190, 152], [230, 177], 10, 2, 128, 33, 1000),
+    "g64": ([60, 40, 1], [60, 300, 80], 64, 1, 64, 1, 300),
+    "long": ([600], [9000], 4, 1, 128, 64, 9001),
+    "ragged": ([70, 3, 129, 1, 64, 500, 0], [71, 3, 640, 2000, 64, 501, 30], 8, 4, 64, 100, 2500),
+    "all_at_once": ([2000], [2000], 4, 2, 64, 64, 2000),
+}
+
+
+@pytest.mark.parametrize("window", [1, 33, 128, 700])
+@pytest.mark.parametrize("shape", SA_TILE_SHAPES)
+@pytest.mark.parametrize("path", ["sa", "gated"])
+def test_sa_tiles(path, shape, window):
+    """Chunks whose SA path goes to the tiles (and, among them, requests that
+    do not)."""
+    new, total, hq, hkv, d, page, cap = SA_TILE_SHAPES[shape]
+    b = Batch(new, total, hq, hkv, d, page, seed=window + len(shape), perm_len=cap, behind=2,
+              shared_perm=window == 33, stride_q=64, pair_pages=window == 128)
+    out = torch.full((b.t + 2, hq, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    err = err_word()
+    b.run(path, window, 77, out=out, err=err, max_new=max(new))
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(out, path, window, 77, weight_bits=8, what=f"{path} {shape}")
+    assert (out[b.t:] == 2.0).all()
+    again = b.run(path, window, 77)
+    assert torch.equal(out[:b.t], again[:b.t])
+
+
+def test_sa_tiles_with_bad_sigma_and_pages():
+    b = Batch([200], [500], 4, 2, 64, 16, seed=2, perm_len=600)
+    good = b.run("sa", 64).clone()
+    table = b.args[3].clone()
+    table[0, 3] = -5
+    args = list(b.args)
+    args[3] = table
+    err = err_word()
+    out = sa.sa_paged_forward(*args, b.perm_d, b.inv_d, window=64, err=err)
+    assert sa.check_error(err) == sa.SA_ERR_BAD_PERM and torch.isfinite(out).all()
+    for bad in (-1, 600, 1 << 30):  # an entry out of range: rows may be missing, nothing is read out of bounds
+        perm = b.perm_d.clone()
+        perm[0, 17] = bad
+        err = err_word()
+        sa.sa_paged_forward(*b.args, perm, b.inv_d, window=64, err=err)
+        assert sa.check_error(err) == sa.SA_ERR_BAD_PERM
+    perm = b.perm_d.clone()
+    perm[0, perm[0].long() == 450] = 10  # one new token twice missing, another token twice
+    err = err_word()
+    out = sa.sa_paged_forward(*b.args, perm, b.inv_d, window=64, err=err,
+                              out=torch.full_like(good, 5.0))
+    assert sa.check_error(err) == sa.SA_ERR_BAD_PERM
+    assert (out[150] == 5.0).all()  # the missing token's row is left
+    err = err_word()
+    assert torch.equal(sa.sa_paged_forward(*b.args, b.perm_d, b.inv_d, window=64, err=err), good)
+    assert sa.check_error(err) == sa.SA_OK
+
+
+def test_sa_tiles_of_requests_that_claim_the_same_rows():
+    """q_start that goes back: more long requests than rows allow."""
+    b = Batch([200] * 6, [200] * 6, 4, 2, 64, 16, seed=2, perm_len=200)
+    starts = i32([0, 200, 0, 200, 0, 200, 0])
+    args = list(b.args)
+    args[0], args[4] = b.q[:200], starts
+    for path in ("sa", "gated"):
+        err = err_word()
+        b.args = tuple(args)
+        b.gate_sa, b.gate_swa = b.gate_sa[:200].contiguous(), b.gate_swa[:200].contiguous()
+        b.run(path, 64, 64, err=err)
+        assert sa.check_error(err) == sa.SA_ERR_BAD_PERM
+
+
 def test_tiles_whose_reference_rises():
     """Scores that grow along the keys by far more than 2^8 a chunk: O is
     rescaled, and the first chunks' weights vanish."""
@@ -193,7 +265,7 @@ def test_snapped_runs_of_many_units():
     new = [900, 1, 700, 401]
     total = [950, 333, 700, 1000]
     b = Batch(new, total, 16, 16, 64, 32, seed=8, perm_len=1000)
-    b.check(b.run("sa", 20), "sa", 20, what="sa")
+    b.check(b.run("sa", 20, kernel=sa.PAGED_ROWS), "sa", 20, what="sa")
     b.check(b.run("gated", 20, 13, kernel=sa.PAGED_ROWS), "gated", 20, 13, what="gated")
     b.check(b.run("swa", 13, kernel=sa.PAGED_ROWS), "swa", 13, what="swa")
 
