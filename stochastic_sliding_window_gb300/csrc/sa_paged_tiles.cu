@@ -12,12 +12,24 @@
 // only when a chunk exceeds it by more than 2^8.  P is rounded to bf16, the
 // operand type of the second product; sums and O are fp32.
 //
-// What bounds it: the tensor cores, 4 d multiply-adds per row and key in two
-// MMAs of M = 128, N = 128 or d (128 cycles per 16 of K for N = 128).  So a
-// half's MMAs must run while the other half is in its softmax, and the
-// softmax of a half (128 rows x 128 keys) must take no longer than the other
-// half's two MMAs: one thread per row holds the row's 128 scores in
-// registers, one pass, masks only in the chunks that a window's end crosses.
+// What bounds it: the tensor cores, 4 d multiply-adds per row and key.  A half's
+// softmax must run beside the other half's MMAs, and a half's two MMAs of a
+// chunk beside its own softmax; so a chunk's scores are taken in two parts of
+// 64 keys, each with its own barriers, and P V of one part and Q K of the next
+// chunk's part run while the other part is in its softmax.  Masks are applied
+// only in the parts that a window's end crosses.
+//
+// Measured (2048 new tokens at the end of 32768, every key in the window, 32 q
+// heads on 8 kv heads, d = 128: 1.06 PFLOP; 568 us at cuBLAS's burst rate):
+//   one MMA warp, softmax over 128 columns at once         857-880 us
+//   64-key parts, two MMA warps, softmax loop unrolled         935 us
+//   the same, the loop over the parts not unrolled         854-875 us
+//   S of all 128 keys by one MMA of N = 128, P in parts        937 us
+//   the halves taking turns, 16 softmax warps in pairs         882 us
+// The unrolled softmax loop does not fit the instruction cache beside the
+// other roles' code.  What is left between 855 and the tensor cores' time is
+// the chain S -> softmax -> P V -> S of a part (1900 cycles, of which 640 are
+// the MMAs of one half).
 //
 // SA.  In sigma's order -- the request's tokens listed by their place in sigma,
 // those that do not exist yet left out -- every row's window is a run of
@@ -35,17 +47,21 @@
 // and the join kernel merges them in order.  Else a tile belongs to the run
 // it starts in.
 //
-// Roles (12 warps, 168 registers per thread: a softmax thread holds 128 scores):
+// Roles (12 warps):
 //   warp 0      producer: TMA.  A lane takes a page of the chunk and loads its
 //               run of rows in boxes of 64, 16, 4 and 1 rows of 128 bytes; lane
-//               0 loads a tile's Q as one box per 64 columns
-//   warp 1      lane 0 issues every MMA; the warp owns TMEM
-//   warps 4-7   softmax and epilogue of rows 0-127, warps 8-11 of 128-255
-// TMEM (512 columns): S of half h in [128 h, +128), overwritten by its bf16 P
-// in the first 64 of them; O of half h in [256 + d h, +d).
-// Order of the MMAs: for each chunk c of a tile, for h = 0, 1: O_h += P_h V(c-1),
-// then S_h = Q_h K(c) -- one thread, one tensor pipe, which runs MMAs in the order
-// of their issue, so S_h may overwrite the P_h that the MMA before it reads.
+//               0 loads a tile's Q as one box per 64 columns.  (SA: warps 0 and
+//               3, cp.async)
+//   warps 1, 2  the elected lane issues the MMAs of half 0, of half 1; warp 1
+//               owns TMEM
+//   warps 4-11  softmax and epilogue: warp 4 + 4 h + i takes rows 32 i .. of
+//               half h, a row a thread, 64 columns at a time
+// TMEM (512 columns): S of half h in [128 h, +128), each part's overwritten by
+// its bf16 P in the first 32 of its 64 columns; O of half h in [256 + d h, +d).
+// Order of the MMAs of a half: for each chunk c of a tile and part u, O += P V of
+// part u of chunk c - 1, then S = Q K of part u of chunk c -- one thread, one
+// tensor pipe, which runs MMAs in the order of their issue, so S may overwrite
+// the P that the MMA before it reads.
 // Every wait is bounded (SA_ERRBIT_TIMEOUT).
 #include "sa_internal.h"
 #include "sa_tc_common.cuh"
@@ -61,7 +77,8 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 1;
 constexpr int kFirstSoftmaxWarp = 4;
 constexpr int kRows = 2 * kBM;
-constexpr int kKC = 128;            // keys per chunk
+constexpr int kKC = 128;            // keys per chunk: of one load
+constexpr int kSub = 64;            // keys per part of a chunk: of one softmax step
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kCutChunks = 32;      // tiles this long on average may be cut
 constexpr uint32_t kMaxSmem = 232448;
@@ -101,17 +118,19 @@ template <int NS>
 struct Bars {
   enum : uint32_t {
     kQfull = 0,           // Q rows of tile x landed
-    kQfree = 1,           // the last S MMA of tile x done
+    kQfree = 1,           // both halves' last S MMA of tile x done
     kKfull = 2,           // [NS] K rows of chunk c landed
     kKfree = kKfull + NS, // [NS] both S MMAs of chunk c done
     kVfull = kKfree + NS, // [NS]
     kVfree = kVfull + NS, // [NS] both O MMAs of chunk c done
-    kSfull = kVfree + NS, // [h] S of the half's chunk c in TMEM
-    kPfull = kSfull + 2,  // [h] P of the half's chunk c written (4 warps)
-    kPVdone = kPfull + 2, // [h] the half's O MMA of chunk c done
-    kOfree = kPVdone + 2, // [h] the half's O of tile x read out (4 warps)
-    kDrain = kOfree + 2,
-    kNum = kDrain + 1,
+    kSfull = kVfree + NS, // [2 h + u] S of the half's part u of a chunk in TMEM
+    kPfull = kSfull + 4,  // [2 h + u] its P written (4 warps)
+    kPVdone = kPfull + 4, // [2 h + u] its O MMA done
+    kOfree = kPVdone + 4, // [h] the half's O of tile x read out (4 warps)
+    kSegFull = kOfree + 2, // [4] the entry of tile x written
+    kSegFree = kSegFull + 4, // [4] and read by every softmax warp and the MMA warp
+    kDrain = kSegFree + 4, // [h]
+    kNum = kDrain + 2,
   };
 };
 
@@ -133,13 +152,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// MMAs and commits of the warp's elected lane: every lane computes the
+// operands, so that they are warp-uniform values.  kAdd: D is added to.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(kAdd ? 1 : 0)
+      : "memory");
+}
+// A from TMEM (P), B from shared memory (V), D in TMEM (O).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&r)[8]) {
@@ -267,13 +307,11 @@ struct Seg {
 };
 
 // What the other roles need of it, in shared memory (slot: tile number mod 4).
-// Written before the tile's Qfull; a slot is written again four tiles on, when
-// the S MMAs of the third tile after it are done, which follow every softmax
-// warp's read of the second's.
 struct Shared {
   int t0, nt, pos0, lo;  // first token's row, tokens, first position, first key (SA:
                          // t0 is the first member's index, pos0 unused)
   int kvh, c0, c1, nch;
+  int a[2], b[2];        // each half's chunks [a, b) of [c0, c1): those its rows have keys in
   int more;              // another tile part follows
   int join;              // last block that holds a part of a tile cut here
   int pad[2];
@@ -350,13 +388,15 @@ __device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
 template <bool SA>
 __device__ Start find_start(const Params& P) {
   const int lane = threadIdx.x & 31;
-  long long total = 0, tiles = 0;
+  long long total = 0, tiles = 0, first = 0;  // first: chunks of request `lane`
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     if (b0 + lane < P.B) {
       const Request r = load_request<SA>(P, b0 + lane, blockIdx.x == 0);
       if (r.n > 0) {
         const int nt = num_tiles(P, r);
-        total += P.Hkv * chunks_before<SA>(P, r, nt);
+        const long long x = P.Hkv * chunks_before<SA>(P, r, nt);
+        if (b0 == 0) first = x;
+        total += x;
         tiles += (long long)P.Hkv * nt;
       }
     }
@@ -379,8 +419,8 @@ __device__ Start find_start(const Params& P) {
   }
   long long before = 0;
   for (int b0 = 0; b0 < P.B; b0 += 32) {
-    long long x = 0;
-    if (b0 + lane < P.B) {
+    long long x = b0 == 0 ? first : 0;
+    if (b0 > 0 && b0 + lane < P.B) {
       const Request r = load_request<SA>(P, b0 + lane, false);
       if (r.n > 0) x = P.Hkv * chunks_before<SA>(P, r, num_tiles(P, r));
     }
@@ -400,13 +440,21 @@ __device__ Start find_start(const Params& P) {
       const long long per_head = chunks_before<SA>(P, r, nt);
       s.kvh = int(rel / per_head);
       rel -= s.kvh * per_head;
-      int lo = 0, hi = nt - 1;  // the last tile that starts at or before rel
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (chunks_before<SA>(P, r, mid) <= rel) lo = mid; else hi = mid - 1;
+      // the last tile that starts at or before rel: 32 candidates at a time
+      int lo = 0, hi = nt;  // lo starts at or before it, hi does not
+      long long at = 0;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int k = min(lo + lane * step, hi);
+        const long long v = k < hi ? chunks_before<SA>(P, r, k) : rel + 1;
+        const unsigned low = __ballot_sync(0xffffffffu, v <= rel);
+        const int last = 31 - __clz(int(low));  // (lane 0 is lo itself)
+        at = __shfl_sync(0xffffffffu, v, last);
+        hi = min(hi, lo + (last + 1) * step);
+        lo = lo + last * step;
       }
       s.grp = lo;
-      s.tile_off = rel - chunks_before<SA>(P, r, lo);
+      s.tile_off = rel - at;
       break;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
@@ -480,7 +528,7 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
     const int last_col = int(unsigned(hi - 1) / unsigned(P.page));
     auto page_at = [&](int col) { return col <= last_col ? table[col] : -1; };
     int page = page_at(int(unsigned(lo + s.c0 * kKC) / unsigned(P.page)) + lane);
-    if (x > 0 && !(ok = wwait(BR::kQfree, uint32_t(x - 1)))) break;
+    if (x > 3 && !(ok = wwait(BR::kSegFree + (x & 3), uint32_t((x >> 2) - 1)))) break;
     if (lane == 0) {
       Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
       sh->t0 = s.r.q0 + i0;
@@ -491,9 +539,16 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       sh->c0 = s.c0;
       sh->c1 = s.c1;
       sh->nch = s.nch;
+      sh->a[0] = sh->a[1] = sh->b[1] = s.c0;
+      sh->b[0] = s.c1;
+      if (min(P.Bt, s.r.n - i0) * P.g > kBM) sh->b[1] = s.c1;  // else half 1 has no rows
       sh->more = more;
       // a run that ends inside a tile is a full one
       sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
+      mbar_arrive(bars + 8 * (BR::kSegFull + (x & 3)));
+    }
+    if (x > 0 && !(ok = wwait(BR::kQfree, uint32_t(x - 1)))) break;
+    if (lane == 0) {
       // rows of other tokens behind the tile's are computed and not written
       mbar_arrive_expect_tx(bars + 8 * BR::kQfull, uint32_t(P.Bt * P.g) * D * 2);
       for (int kb = 0; kb < D / 64; ++kb)
@@ -604,9 +659,9 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
   __syncwarp();
 }
 
-// SA: rows from anywhere, so cp.async by three warps (96 threads).  The list's
-// entries of a chunk are read one chunk ahead, by one or two keys a thread.
-constexpr int kSaProducers = 96;
+// SA: rows from anywhere, so cp.async by two warps.  The list's entries of a
+// chunk are read one chunk ahead, two keys a thread.
+constexpr int kSaProducers = 64;
 
 template <int D, int NS>
 __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
@@ -616,10 +671,11 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
   constexpr int CPR = D / 8;               // 16-byte chunks per row
   constexpr int RPP = kSaProducers / CPR;  // rows per pass
   const int lane = threadIdx.x & 31;
-  const int tid = threadIdx.x < 32 ? int(threadIdx.x) : int(threadIdx.x) - 32;  // warps 0, 2, 3
+  const int tid = threadIdx.x < 32 ? int(threadIdx.x) : int(threadIdx.x) - 64;  // warps 0 and 3
   const int cc = tid % CPR, r_first = tid / CPR;
   const uint32_t col = uint32_t(cc >> 3) * (kKC * 128), c8 = uint32_t(cc & 7);
   uint32_t* srow = reinterpret_cast<uint32_t*>(smem + P.off_seg + 4 * sizeof(Shared));  // [2][128]
+  int* sq = reinterpret_cast<int*>(srow + 2 * kKC);  // [256] the tile's query rows
   int step = 0;
   // every producer learns whether thread 0's wait succeeded; also orders
   // their shared-memory writes before what follows
@@ -633,15 +689,25 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
   };
   const char* kbase = reinterpret_cast<const char*>(P.k) + cc * 16;
   const char* vbase = reinterpret_cast<const char*>(P.v) + cc * 16;
+  // row numbers of several keys first, then their copies (the copies' asm
+  // would hold the shared-memory reads back)
   auto rows_in = [&](const char* base, uint32_t dst, const uint32_t* rows) {
-#pragma unroll 6
-    for (int i = r_first; i < kKC; i += RPP) {
-      const uint32_t r = rows[i];
-      const uint32_t to = dst + uint32_t(i) * 128 + ((c8 ^ uint32_t(i & 7)) << 4);
-      const int bytes = r != 0xffffffffu ? 16 : 0;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                   "l"(base + uint64_t(bytes ? r : 0u) * (D * 2)), "r"(bytes)
-                   : "memory");
+    constexpr int kBatch = 8;
+    for (int i0 = r_first; i0 < kKC; i0 += RPP * kBatch) {
+      uint32_t r[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) r[u] = i0 + u * RPP < kKC ? rows[i0 + u * RPP] : 0u;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * RPP;
+        if (i < kKC) {
+          const int bytes = r[u] != 0xffffffffu ? 16 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           dst + uint32_t(i) * 128 + ((c8 ^ uint32_t(i & 7)) << 4)),
+                       "l"(base + uint64_t(bytes ? r[u] : 0u) * (D * 2)), "r"(bytes)
+                       : "memory");
+        }
+      }
     }
   };
   Cursor cur = make_cursor<true>(P, start);
@@ -660,28 +726,61 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
       const int j = lo + c * kKC + at;
       return j < hi ? list[j] : make_uint2(0xffffffffu, 0x7fffffffu);
     };
-    const bool two = tid < kKC - kSaProducers;
-    uint2 e0 = entry(s.c0, tid), e1 = two ? entry(s.c0, kSaProducers + tid) : make_uint2(0u, 0u);
-    if (!(ok = agree(BR::kQfree, uint32_t(x - 1), x > 0))) break;
+    uint2 e0 = entry(s.c0, tid), e1 = entry(s.c0, kSaProducers + tid);
+    const bool entry_used = x > 3;
     if (tid == 0) {
-      Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
-      sh->t0 = m0;
-      sh->nt = nt;
-      sh->pos0 = 0;
-      sh->lo = lo;
-      sh->kvh = s.kvh;
-      sh->c0 = s.c0;
-      sh->c1 = s.c1;
-      sh->nch = s.nch;
-      sh->more = more;
-      sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
-      mbar_arrive(bars + 8 * BR::kQfull);
+      // each half's chunks: from its first member's window to its last one's
+      int a[2], b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a[h] = b[h] = s.c0;
+        const int rows = min(nt * P.g, (h + 1) * kBM) - h * kBM;
+        if (rows > 0) {
+          const int first = P.order.members[m0 + h * kBM / P.g].x;
+          const int last = P.order.members[m0 + (h * kBM + rows - 1) / P.g].y;
+          a[h] = max(s.c0, (first - lo) / kKC);
+          b[h] = max(a[h], min(s.c1, (last - lo) / kKC + 1));
+        }
+      }
+      if (!entry_used || bounded_wait(bars + 8 * (BR::kSegFree + (x & 3)), uint32_t((x >> 2) - 1) & 1u,
+                                      P.timeout_cycles, P.err, abort_flag)) {
+        Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
+        sh->t0 = m0;
+        sh->nt = nt;
+        sh->pos0 = 0;
+        sh->lo = lo;
+        sh->kvh = s.kvh;
+        sh->c0 = s.c0;
+        sh->c1 = s.c1;
+        sh->nch = s.nch;
+        for (int h = 0; h < 2; ++h) {
+          sh->a[h] = a[h];
+          sh->b[h] = b[h];
+        }
+        sh->more = more;
+        sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
+        mbar_arrive(bars + 8 * (BR::kSegFull + (x & 3)));
+      }
     }
-    for (int r = r_first; r < nt * P.g; r += RPP) {
-      const int t = r / P.g, j = r - t * P.g;
-      const int row = P.order.members[m0 + t].z;
-      cp_async16(sbase + uint32_t(cc >> 3) * (kRows * 128) + uint32_t(r) * 128 + ((c8 ^ uint32_t(r & 7)) << 4),
-                 P.q + (long long)row * P.q_stride + (s.kvh * P.g + j) * D + cc * 8);
+    for (int t = tid; t < nt; t += kSaProducers) sq[t] = P.order.members[m0 + t].z;
+    if (!(ok = agree(BR::kQfree, uint32_t(x - 1), x > 0))) break;
+    {
+      constexpr int kBatch = 8;
+      const int rows = nt * P.g;
+      for (int i0 = r_first; i0 < rows; i0 += RPP * kBatch) {
+        const __nv_bfloat16* src[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int r = min(i0 + u * RPP, rows - 1), t = r / P.g;
+          src[u] = P.q + (long long)sq[t] * P.q_stride + (s.kvh * P.g + r - t * P.g) * D + cc * 8;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const uint32_t r = uint32_t(i0 + u * RPP);
+          if (int(r) < rows)
+            cp_async16(sbase + uint32_t(cc >> 3) * (kRows * 128) + r * 128 + ((c8 ^ (r & 7)) << 4), src[u]);
+        }
+      }
     }
     cp_async_arrive_noinc(bars + 8 * BR::kQfull);
     for (int c = s.c0; c < s.c1; ++c, ++n) {
@@ -700,14 +799,14 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
         }
       };
       put(tid, e0);
-      if (two) put(kSaProducers + tid, e1);
+      put(kSaProducers + tid, e1);
       if (tid == 0) {
         keys->good = 1;  // rows that are not there are zeros
         keys->steps = kKC / 16;
       }
       if (c + 1 < s.c1) {
         e0 = entry(c + 1, tid);
-        if (two) e1 = entry(c + 1, kSaProducers + tid);
+        e1 = entry(c + 1, kSaProducers + tid);
       }
       if (!(ok = agree(BR::kKfree + st, uint32_t(n / NS - 1), n >= NS))) break;
       rows_in(kbase, sbase + P.off_k + uint32_t(st) * kTile + col, rows);
@@ -723,84 +822,111 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
 
 // ------------------------------------------------------------------ MMA issue
 template <int D, int NS, bool SA>
-__device__ void mma_role(const Params& P, bool more, const Shared* seg, const typename KeysOf<SA>::T* keys,
+__device__ void mma_role(const Params& P, int h, bool more, const Shared* seg, const typename KeysOf<SA>::T* keys,
                          uint32_t sbase, uint32_t tmem, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
-  const uint32_t idesc_qk = idesc_bf16(kBM, kKC, 0), idesc_pv = idesc_bf16(kBM, D, 1);
+  constexpr uint32_t kIdescQk = idesc_bf16(kBM, kSub, 0), kIdescPv = idesc_bf16(kBM, D, 1);
+  constexpr uint32_t kSubRows = kSub * 128 / 16;  // descriptor units between a chunk's parts
   // Q: column blocks of [256 rows x 128 B], half h from row 128 h
-  const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + kBM * 128, 16, 1024)};
+  const uint64_t qd = sdesc_sw128(sbase + uint32_t(h) * (kBM * 128), 16, 1024);
   const uint64_t kd = sdesc_sw128(sbase + P.off_k, 16, 1024);
   const uint64_t vd = sdesc_sw128(sbase + P.off_v, kKC * 128, 1024);
+  const uint32_t ts = tmem + uint32_t(h * kKC), to = tmem + uint32_t(2 * kKC + h * D);
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    return bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
+    const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
+    return __all_sync(0xffffffffu, ok);
   };
-  // O_h (+)= P_h V of chunk number n, tile number x; add: O holds the sum of
-  // earlier chunks (one of whose keys, at least, is real: the V rows standing
-  // in for bad pages only may hold anything, and what they gave is dropped)
-  auto pv = [&](int h, int n, int x, bool first, bool add, int steps) {
-    if (!wait(BR::kPfull + h, uint32_t(n))) return false;
-    if (h == 0 && !wait(BR::kVfull + n % NS, uint32_t(n / NS))) return false;
-    if (first && x > 0 && !wait(BR::kOfree + h, uint32_t(x - 1))) return false;
+  int np[2] = {0, 0}, xh = 0;  // O MMAs of each part, tile parts so far
+  auto pv_ready = [&](int u, bool first) {
+    return wait(BR::kPfull + 2 * h + u, uint32_t(np[u]++)) &&
+           !(first && xh > 0 && !wait(BR::kOfree + h, uint32_t(xh - 1)));
+  };
+  // O (+)= P V of part u of chunk number n, `steps` times 16 keys.  add: O holds
+  // the sum of earlier parts (one of whose keys, at least, is real: the V rows
+  // standing in for bad pages only may hold anything, and what they gave is
+  // dropped).
+  auto pv = [&](int n, int u, bool add, int steps) {
     if (SA) fence_proxy_async_smem();  // cp.async (generic proxy) data -> tensor core reads
     tc_fence_after();
-    const uint32_t o = tmem + uint32_t(2 * kKC + h * D), p = tmem + uint32_t(h * kKC);
-    const uint64_t b = vd + uint64_t(n % NS) * (kTile / 16);
-    if (steps == kKC / 16) {
+    const uint64_t b = vd + uint64_t(n % NS) * (kTile / 16) + uint32_t(u) * kSubRows;
+    const uint32_t p = ts + uint32_t(u * kSub);
+    if (steps == kSub / 16) {
+      mma_ts(to, p, b, kIdescPv, add ? 1u : 0u);
 #pragma unroll
-      for (int kk = 0; kk < kKC / 16; ++kk)
-        umma_bf16_ts(o, p + 8 * kk, b + 128 * kk, idesc_pv, (add || kk > 0) ? 1u : 0u);  // 16 keys of 128 B
+      for (int kk = 1; kk < kSub / 16; ++kk) mma_ts(to, p + 8 * kk, b + 128 * kk, kIdescPv, 1u);  // 16 keys of 128 B
     } else {
-      for (int kk = 0; kk < steps; ++kk)
-        umma_bf16_ts(o, p + 8 * kk, b + 128 * kk, idesc_pv, (add || kk > 0) ? 1u : 0u);
+      for (int kk = 0; kk < steps; ++kk) mma_ts(to, p + 8 * kk, b + 128 * kk, kIdescPv, (add || kk > 0) ? 1u : 0u);
     }
-    umma_commit(bars + 8 * (BR::kPVdone + h));
-    if (h == 1) umma_commit(bars + 8 * (BR::kVfree + n % NS));
-    return true;
+    commit_elected(bars + 8 * (BR::kPVdone + 2 * h + u));
   };
-  auto qk = [&](int h, int n, bool last) {
+  auto qk = [&](int n, int u) {
     if (SA) fence_proxy_async_smem();
     tc_fence_after();
-    const uint32_t d = tmem + uint32_t(h * kKC);
-    const uint64_t b0 = kd + uint64_t(n % NS) * (kTile / 16);
+    const uint64_t b = kd + uint64_t(n % NS) * (kTile / 16) + uint32_t(u) * kSubRows;
+    const uint32_t d = ts + uint32_t(u * kSub);
+    mma_ss<false>(d, qd, b, kIdescQk);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const uint64_t da = uint64_t((kk >> 2) * (kRows * 128 / 16) + (kk & 3) * 2);
-      const uint64_t db = uint64_t((kk >> 2) * (kKC * 128 / 16) + (kk & 3) * 2);
-      umma_bf16(d, qd[h] + da, b0 + db, idesc_qk, kk > 0 ? 1u : 0u);
-    }
-    umma_commit(bars + 8 * (BR::kSfull + h));
-    if (h == 1) {
-      umma_commit(bars + 8 * (BR::kKfree + n % NS));
-      if (last) umma_commit(bars + 8 * BR::kQfree);
-    }
+    for (int kk = 1; kk < D / 16; ++kk)
+      mma_ss<true>(d, qd + uint64_t((kk >> 2) * (kRows * 128 / 16) + (kk & 3) * 2),
+                   b + uint64_t((kk >> 2) * (kKC * 128 / 16) + (kk & 3) * 2), kIdescQk);
+    commit_elected(bars + 8 * (BR::kSfull + 2 * h + u));
   };
-  int n = 0, x = 0;
+  int n = 0;
   bool ok = true;
-  for (; ok && more; ++x) {
-    if (!(ok = wait(BR::kQfull, uint32_t(x)))) break;
+  for (int x = 0; ok && more; ++x) {
+    if (!(ok = wait(BR::kSegFull + (x & 3), uint32_t(x >> 2)))) break;
     const Shared* sh = seg + (x & 3);
-    const int chunks = sh->c1 - sh->c0;
-    more = sh->more != 0;
-    bool add = false;
+    const int c0 = sh->c0;
+    const int chunks = __shfl_sync(0xffffffffu, sh->c1 - c0, 0);
+    const int a = __shfl_sync(0xffffffffu, sh->a[h] - c0, 0), b = __shfl_sync(0xffffffffu, sh->b[h] - c0, 0);
+    more = __shfl_sync(0xffffffffu, sh->more, 0) != 0;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (BR::kSegFree + (x & 3)));
+    if (!(ok = wait(BR::kQfull, uint32_t(x)))) break;
+    bool good = false;  // some key up to the chunk before this one is real
+    // (chunks the half has no part in are only waited for and given back)
+    int parts = 2;      // of the current chunk
     for (int c = 0; ok && c < chunks; ++c, ++n) {
-      ok = wait(BR::kKfull + n % NS, uint32_t(n / NS));
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (ok && c > 0) ok = pv(h, n - 1, x, c == 1, add, kKC / 16);
-        if (ok) qk(h, n, c == chunks - 1);
+      const bool o = c > a && c <= b, sc = c >= a && c < b;  // O MMAs of chunk c - 1, S MMAs of chunk c
+      bool good_last = true;
+      if (c > 0) {
+        ok = wait(BR::kVfull + (n - 1) % NS, uint32_t((n - 1) / NS));
+        if (!SA && !good) good_last = __shfl_sync(0xffffffffu, keys[(n - 1) % kKeySlots].good, 0) != 0;
       }
-      if (c > 0) add = keys[(n - 1) % kKeySlots].good != 0;
+      if (ok) ok = wait(BR::kKfull + n % NS, uint32_t(n / NS));
+      if (!SA && c == chunks - 1) parts = (__shfl_sync(0xffffffffu, keys[n % kKeySlots].steps, 0) + 3) / 4;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (ok && o && (ok = pv_ready(u, u == 0 && c - 1 == a)))
+          pv(n - 1, u, u == 0 ? c - 1 > a && good : good_last, kSub / 16);
+        if (ok && sc && u < parts) qk(n, u);
+      }
+      if (ok) {
+        if (c > 0) commit_elected(bars + 8 * (BR::kVfree + (n - 1) % NS));
+        commit_elected(bars + 8 * (BR::kKfree + n % NS));
+        if (c == chunks - 1) commit_elected(bars + 8 * BR::kQfree);
+      }
+      if (c > 0) good = good_last;
     }
     // the last O MMAs do not wait for the next tile's operands
-    const int steps = keys[(n - 1) % kKeySlots].steps;  // (earlier chunks are full)
-    if (ok) ok = pv(0, n - 1, x, chunks == 1, add, steps);
-    if (ok) ok = pv(1, n - 1, x, chunks == 1, add, steps);
+    if (ok) ok = wait(BR::kVfull + (n - 1) % NS, uint32_t((n - 1) / NS));
+    if (ok && b > a && b == chunks) {
+      const bool good_last = SA || good || __shfl_sync(0xffffffffu, keys[(n - 1) % kKeySlots].good, 0) != 0;
+      // (earlier chunks are full)
+      const int steps = SA ? kKC / 16 : __shfl_sync(0xffffffffu, keys[(n - 1) % kKeySlots].steps, 0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (ok && u < parts && (ok = pv_ready(u, u == 0 && chunks - 1 == a)))
+          pv(n - 1, u, u == 0 ? chunks - 1 > a && good : good_last, min(kSub / 16, steps - u * (kSub / 16)));
+    }
+    if (b > a) ++xh;
+    if (ok) commit_elected(bars + 8 * (BR::kVfree + (n - 1) % NS));
   }
-  umma_commit(bars + 8 * BR::kDrain);
+  commit_elected(bars + 8 * (BR::kDrain + h));
   const long long t0 = clock64();
-  while (!mbar_try_wait(bars + 8 * BR::kDrain, 0) && clock64() - t0 < kDrainCycles) {
+  while (!mbar_try_wait(bars + 8 * (BR::kDrain + h), 0) && clock64() - t0 < kDrainCycles) {
   }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
@@ -815,19 +941,18 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
   const uint32_t lanes = uint32_t(quad * 32) << 16;
   const uint32_t sb = tmem + lanes + uint32_t(h * kKC);
   const uint32_t ob = tmem + lanes + uint32_t(2 * kKC + h * D);
-  auto wwait = [&](uint32_t bar, uint32_t parity) {
+  auto wait = [&](uint32_t bar, uint32_t parity) {
     const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
     return __all_sync(0xffffffffu, ok);
   };
   const uint64_t sl2 = f2_pack(P.scale_log2, P.scale_log2);
-  int n = 0, x = 0;
-  while (more) {
-    // the tile's first S also says that its entry in shared memory is there
-    if (!wwait(BR::kSfull + h, uint32_t(n))) return;
+  int nbase = 0;         // chunks of earlier tile parts
+  int k[2] = {0, 0};     // this half's S of each part so far
+  for (int x = 0; more; ++x) {
+    if (!wait(BR::kSegFull + (x & 3), uint32_t(x >> 2))) return;
     const Shared* sh = seg + (x & 3);
-    ++x;
     more = sh->more != 0;
-    const int c0 = sh->c0, c1 = sh->c1;
+    const int c0 = sh->c0, c1 = sh->c1, a = sh->a[h], b = sh->b[h];
     const bool live = t < sh->nt;
     int4 mem = make_int4(0, -1, 0, 0);
     if (SA && live) mem = P.order.members[sh->t0 + t];
@@ -838,7 +963,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
     const bool whole = c0 == 0 && c1 == sh->nch;
     const int slot = int(blockIdx.x) * 2 + (c0 == 0 ? 1 : 0);
     const size_t orow = live ? size_t(SA ? mem.z : sh->t0 + t) * P.Hq + size_t(sh->kvh) * P.g + j : 0;
-    if (sh->join >= 0 && h == 0 && quad == 0 && lane == 0) {
+    if (sh->join >= 0 && warp == kFirstSoftmaxWarp && lane == 0) {
       Desc d;
       d.valid = 1;
       d.c1 = sh->join;
@@ -848,107 +973,128 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
       d.pad = 0;
       P.desc[blockIdx.x] = d;
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (BR::kSegFree + (x & 3)));
     float ref = -INFINITY, l = 0.f;
-    for (int c = c0; c < c1; ++c, ++n) {
-      if (c > c0 && !wwait(BR::kSfull + h, uint32_t(n))) return;
-      tc_fence_after();
-      uint32_t v[4][32];
+    int last_u = 0;
+    for (int c = a; c < b; ++c) {
+      const auto& key = keys[(nbase + c - c0) % kKeySlots];
+      int parts = 2;
+#pragma unroll 1  // (unrolled: slower by 8 %, see the top)
+      for (int u = 0; u < 2; ++u) {
+        if (u >= parts) break;
+        if (!wait(BR::kSfull + 2 * h + u, uint32_t(k[u]))) return;
+        tc_fence_after();
+        uint32_t v[2][32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32_async(sb + q * 32, v[q]);
-      const uint4 bad = *reinterpret_cast<const uint4*>(keys[n % kKeySlots].bad);
-      const int lo = klo - c * kKC, hi = khi - c * kKC;
-      bool clear = lo <= 0 && hi >= kKC - 1 && (bad.x | bad.y | bad.z | bad.w) == 0u;
-      uint4 fresh = make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (SA) {
-        fresh = *reinterpret_cast<const uint4*>(keys[n % kKeySlots].fresh);
-        clear = clear && (fresh.x | fresh.y | fresh.z | fresh.w) == 0u;
-      }
-      tmem_wait_ld();
+        for (int q = 0; q < 2; ++q) tmem_ld32_async(sb + u * kSub + q * 32, v[q]);
+        // (a chunk's words are there before its first S)
+        if (!SA && u == 0 && c == c1 - 1) parts = (key.steps + 3) / 4;
+        const uint2 bad = *reinterpret_cast<const uint2*>(&key.bad[2 * u]);
+        const int lo = klo - c * kKC - u * kSub, hi = khi - c * kKC - u * kSub;
+        bool clear = lo <= 0 && hi >= kSub - 1 && (bad.x | bad.y) == 0u;
+        uint2 fresh = make_uint2(0u, 0u);
+        if constexpr (SA) {
+          fresh = *reinterpret_cast<const uint2*>(&key.fresh[2 * u]);
+          clear = clear && (fresh.x | fresh.y) == 0u;
+        }
+        tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) reg_fence(v[q]);
-      if (!__all_sync(0xffffffffu, clear)) {
-        const uint32_t bw[4] = {bad.x, bad.y, bad.z, bad.w};
+        for (int q = 0; q < 2; ++q) reg_fence(v[q]);
+        if (!__all_sync(0xffffffffu, clear)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t keep = band_bits(lo, hi, q * 32) & ~bw[q];
-          if constexpr (SA) {  // of the new tokens, the later ones are left out
-            const uint32_t fw[4] = {fresh.x, fresh.y, fresh.z, fresh.w};
-            for (uint32_t f = fw[q]; f != 0u; f &= f - 1u) {
-              const int e = __ffs(int(f)) - 1;
-              if (keys[n % kKeySlots].toks[q * 32 + e] > pos) keep &= ~(1u << e);
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t keep = band_bits(lo, hi, q * 32) & ~(q == 0 ? bad.x : bad.y);
+            if (!__all_sync(0xffffffffu, keep == 0xffffffffu)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((keep >> e) & 1u)) v[q][e] = __float_as_uint(-INFINITY);
+            }
+            if constexpr (SA) {  // of the new tokens, the later ones are left out
+              if ((q == 0 ? fresh.x : fresh.y) != 0u) {
+                const int4* tk = reinterpret_cast<const int4*>(key.toks + u * kSub + q * 32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int4 y = tk[e];
+                  if (y.x > pos) v[q][4 * e] = __float_as_uint(-INFINITY);
+                  if (y.y > pos) v[q][4 * e + 1] = __float_as_uint(-INFINITY);
+                  if (y.z > pos) v[q][4 * e + 2] = __float_as_uint(-INFINITY);
+                  if (y.w > pos) v[q][4 * e + 3] = __float_as_uint(-INFINITY);
+                }
+              }
             }
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((keep >> e) & 1u)) v[q][e] = __float_as_uint(-INFINITY);
         }
-      }
-      float mx[4];
+        float mx[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mx[q] = __uint_as_float(v[q][0]);
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t* y = &v[q >> 1][16 * (q & 1)];
+          mx[q] = __uint_as_float(y[0]);
 #pragma unroll
-        for (int e = 1; e + 1 < 32; e += 2)
-          mx[q] = fmax3(mx[q], __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
-        mx[q] = fmaxf(mx[q], __uint_as_float(v[q][31]));
-      }
-      const float msc = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * P.scale_log2;
-      float alpha = 1.f;
-      bool rescale = false;
-      if (ref == -INFINITY) {
-        ref = msc;  // nothing attended before: O and l are still 0 for this row
-      } else if (msc > ref + kRescaleLog2) {
-        alpha = fast_exp2(ref - msc);
-        ref = msc;
-        l *= alpha;
-        rescale = true;
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
-        // O must hold the O MMAs of every earlier chunk of the tile
-        if (!wwait(BR::kPVdone + h, uint32_t(n - 1))) return;
-        tc_fence_after();
+          for (int e = 1; e + 1 < 16; e += 2) mx[q] = fmax3(mx[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(y[15]));
+        }
+        const float msc = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * P.scale_log2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (ref == -INFINITY) {
+          ref = msc;  // nothing attended before: O and l are still 0 for this row
+        } else if (msc > ref + kRescaleLog2) {
+          alpha = fast_exp2(ref - msc);
+          ref = msc;
+          l *= alpha;
+          rescale = true;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O must hold the O MMAs of every earlier part: they finish in order
+          if (!wait(BR::kPVdone + 2 * h + (u ^ 1), uint32_t(u == 1 ? k[0] - 1 : k[1] - 1))) return;
+          tc_fence_after();
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
-          uint32_t o[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-              "%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]),
-                "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-              : "r"(ob + q * 16)
-              : "memory");
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                "%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]),
+                  "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                : "r"(ob + q * 16)
+                : "memory");
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st16(ob + q * 16, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(ob + q * 16, o);
+          }
+          tmem_wait_st();
         }
+        const float nref = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t nms = f2_pack(nref, nref);
+        uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = f2_unpack(f2_fma(
+                f2_pack(__uint_as_float(v[q][2 * e]), __uint_as_float(v[q][2 * e + 1])), sl2, nms));
+            const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+            acc[e & 1] = f2_add(acc[e & 1], f2_pack(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(sb + u * kSub + q * 16, pk);
+        }
+        const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
+        l += (a0.x + a0.y) + (a1.x + a1.y);
         tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (BR::kPfull + 2 * h + u));
+        ++k[u];
+        last_u = u;
       }
-      const float nref = ref == -INFINITY ? 0.f : -ref;
-      const uint64_t nms = f2_pack(nref, nref);
-      uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = f2_unpack(f2_fma(
-              f2_pack(__uint_as_float(v[q][2 * e]), __uint_as_float(v[q][2 * e + 1])), sl2, nms));
-          const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
-          acc[e & 1] = f2_add(acc[e & 1], f2_pack(p0, p1));
-          pk[e] = pack_bf16x2(p0, p1);
-        }
-        tmem_st16(sb + q * 16, pk);
-      }
-      const float2 a0 = f2_unpack(acc[0]), a1 = f2_unpack(acc[1]);
-      l += (a0.x + a0.y) + (a1.x + a1.y);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (BR::kPfull + h));
     }
-    // epilogue: the tile's part is done when its last O MMA is
-    if (!wwait(BR::kPVdone + h, uint32_t(n - 1))) return;
+    nbase += c1 - c0;
+    // epilogue: the tile part is done when its last O MMA is
+    if (b > a && !wait(BR::kPVdone + 2 * h + last_u, uint32_t(k[last_u] - 1))) return;
     tc_fence_after();
     float mul = l == 0.f ? 0.f : 1.f / l;
     if (P.gate != nullptr && live) mul *= 1.f / (1.f + expf(-P.gate[orow]));
@@ -956,18 +1102,19 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       uint32_t o[32];
-      tmem_ld32(ob + q * 32, o);
-      if (l == 0.f) {  // a row without keys is 0, whatever bad pages left in O
+      const int col = q * 32;
+      tmem_ld32(ob + col, o);
+      if (l == 0.f || b <= a) {  // a row without keys is 0, whatever bad pages left in O
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      if (q == D / 32 - 1) {
+      if (q == D / 32 - 1 && b > a) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (BR::kOfree + h));
       }
       if (!whole) {
-        float4* dst = reinterpret_cast<float4*>(P.part) + (size_t(slot) * (D / 4) + q * 8) * kRows + row;
+        float4* dst = reinterpret_cast<float4*>(P.part) + (size_t(slot) * (D / 4) + col / 4) * kRows + row;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           dst[e * kRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
@@ -980,7 +1127,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
           o[2 * e + 1] = __float_as_uint(y.y);
         }
         if (SA && P.swa_part != nullptr) {
-          const float4* add = reinterpret_cast<const float4*>(P.swa_part + orow * D + q * 32);
+          const float4* add = reinterpret_cast<const float4*>(P.swa_part + orow * D + col);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 y = add[e];
@@ -996,7 +1143,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
             uint32_t w[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) w[u] = o[8 * e + u];
-            st_global_v8(P.part_out + orow * D + q * 32 + e * 8, w);
+            st_global_v8(P.part_out + orow * D + col + e * 8, w);
           }
         } else {
 #pragma unroll
@@ -1005,7 +1152,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
 #pragma unroll
             for (int u = 0; u < 8; ++u)
               w[u] = pack_bf16x2(__uint_as_float(o[16 * e + 2 * u]), __uint_as_float(o[16 * e + 2 * u + 1]));
-            st_global_2v4(P.out + orow * D + q * 32 + e * 16, w);
+            st_global_2v4(P.out + orow * D + col + e * 16, w);
           }
         }
       }
@@ -1030,6 +1177,44 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P.off_bar + 8 * BR::kNum);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P.off_bar + 8 * BR::kNum + 4);
   const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 64) {
+    mbar_init(bars + 8 * BR::kQfull, SA ? kSaProducers : 1);
+    mbar_init(bars + 8 * BR::kQfree, 2);
+    for (int i = 0; i < NS; ++i) {
+      // SA: the producers' copies, and thread 0 for the key words
+      mbar_init(bars + 8 * (BR::kKfull + i), SA ? kSaProducers + 1 : 1);
+      mbar_init(bars + 8 * (BR::kKfree + i), 2);
+      mbar_init(bars + 8 * (BR::kVfull + i), SA ? kSaProducers : 1);
+      mbar_init(bars + 8 * (BR::kVfree + i), 2);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(bars + 8 * (BR::kOfree + h), 4);
+      mbar_init(bars + 8 * (BR::kDrain + h), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bars + 8 * (BR::kSegFull + i), 1);
+      mbar_init(bars + 8 * (BR::kSegFree + i), 8 + 2);
+      mbar_init(bars + 8 * (BR::kSfull + i), 1);
+      mbar_init(bars + 8 * (BR::kPfull + i), 4);
+      mbar_init(bars + 8 * (BR::kPVdone + i), 1);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // SA: this much may run beside the order kernel (and whatever went before it);
+  // SWA: the order kernel may run beside the rest.
+  if (SA) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  if (threadIdx.x == 64 && P.desc != nullptr) P.desc[blockIdx.x].valid = 0;
   if (warp == 0) {
     const Start s = find_start<SA>(P);
     Cursor cur = make_cursor<SA>(P, s);
@@ -1039,32 +1224,6 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
       s_start = s;
       s_any = any;
     }
-  } else if (threadIdx.x == 64) {
-    // SA: the producers' copies, and thread 0 for what it and they wrote besides
-    mbar_init(bars + 8 * BR::kQfull, SA ? kSaProducers + 1 : 1);
-    mbar_init(bars + 8 * BR::kQfree, 1);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(bars + 8 * (BR::kKfull + i), SA ? kSaProducers + 1 : 1);
-      mbar_init(bars + 8 * (BR::kKfree + i), 1);
-      mbar_init(bars + 8 * (BR::kVfull + i), SA ? kSaProducers : 1);
-      mbar_init(bars + 8 * (BR::kVfree + i), 1);
-    }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(bars + 8 * (BR::kSfull + h), 1);
-      mbar_init(bars + 8 * (BR::kPfull + h), 4);
-      mbar_init(bars + 8 * (BR::kPVdone + h), 1);
-      mbar_init(bars + 8 * (BR::kOfree + h), 4);
-    }
-    mbar_init(bars + 8 * BR::kDrain, 1);
-    *abort_flag = 0;
-    if (P.desc != nullptr) P.desc[blockIdx.x].valid = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  } else if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_slot)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -1076,9 +1235,8 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
 
   if (warp >= kFirstSoftmaxWarp) {
     softmax_role<D, NS, SA>(P, any, seg, keys, tmem, bars, abort_flag);
-  } else if (warp == kMmaWarp) {
-    if ((threadIdx.x & 31) == 0) mma_role<D, NS, SA>(P, any, seg, keys, sbase, tmem, bars, abort_flag);
-    __syncwarp();
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    mma_role<D, NS, SA>(P, warp - kMmaWarp, any, seg, keys, sbase, tmem, bars, abort_flag);
   } else if (SA) {
     sa_producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, s_vote);
   } else if (warp == 0) {
@@ -1176,14 +1334,24 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
   P.off_v = P.off_k + NS * tile;
   P.off_bad = P.off_v + NS * tile;
   P.off_seg = P.off_bad + kKeySlots * uint32_t(sizeof(K));
-  P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared)) + (SA ? 2 * kKC * 4 : 0);
+  P.off_bar = P.off_seg + 4 * uint32_t(sizeof(Shared)) + (SA ? (2 * kKC + kRows) * 4 : 0);
   const uint32_t smem = P.off_bar + 8 * Bars<NS>::kNum + 16 + 1024;
-  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(K) + 4 * sizeof(Shared) + 2 * kKC * 4 + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
+  static_assert(2 * kBM * D * 2 + 2 * NS * kKC * D * 2 + kKeySlots * sizeof(K) + 4 * sizeof(Shared) + (2 * kKC + kRows) * 4 + 128 + 8 * Bars<NS>::kNum + 16 + 1024 + 64 <=
                     kMaxSmem, "shared memory");
   cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS, SA>>(smem);
   if (ce != cudaSuccess) return ce;
-  sa_paged_tiles_kernel<D, NS, SA><<<sms, kThreads, smem, stream>>>(P);
-  if ((ce = cudaGetLastError()) != cudaSuccess || P.desc == nullptr) return ce;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = SA ? 1 : 0;
+  ce = cudaLaunchKernelEx(&cfg, sa_paged_tiles_kernel<D, NS, SA>, P);
+  if (ce != cudaSuccess || P.desc == nullptr) return ce;
   sa_paged_tiles_join_kernel<D, SA><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
   return cudaGetLastError();
 }

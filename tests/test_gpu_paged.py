@@ -202,9 +202,9 @@ def test_tiles_with_bad_pages_and_lengths():
 def test_tile_waits_give_up_within_their_bound():
     """A wait limit far below a chunk's time: the call returns with the
     timeout bit, the context stays usable."""
-    b = Batch([300], [3000], 8, 2, 128, 16, seed=1)
+    b = Batch([300], [3000], 8, 2, 128, 1, seed=1)  # pages of one token: the slowest loads
     err = err_word()
-    sa.set_wait_limit(50)
+    sa.set_wait_limit(1)
     try:
         b.run("swa", ALL, kernel=sa.PAGED_TILES, err=err)
         assert sa.check_error(err) == sa.SA_ERR_TIMEOUT
