@@ -198,7 +198,6 @@ int paged_tile_tokens(const PagedProblem& pb);  // tokens of a tile
 struct SaOrder {
   uint2* list;     // [requests taken][cap] tokens in sigma's order: row of the
                    // caches at kv head 0 (0xffffffff: bad page), position
-  int32_t* place;  // the same: places in sigma
   int4* members;   // [T] new tokens in sigma's order, a request's from q_start on:
                    // first and last list entry of the window, row, position
   int32_t* chunks; // [T + B] key chunks before each of a request's tiles, from q_start + b on
@@ -210,9 +209,12 @@ struct SaOrder {
 __host__ __device__ inline bool paged_sa_tiled(int n, int len, int half, int row_limit) {
   return n > row_limit && (long long)n * (2LL * half + 1) >= len;
 }
+inline bool paged_order_supported(const PagedProblem& pb) { return pb.B <= 1 << 27; }  // eight blocks each
 size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit);
+// beside: the kernel before it in the stream is the SWA tile kernel of the same
+// call (or its join), beside which it may run.
 sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_tokens, void* workspace,
-                               SaOrder* order, cudaStream_t stream);
+                               SaOrder* order, bool beside, cudaStream_t stream);
 sa_status_t launch_paged_sa_tiles(const PagedProblem& pb, const SaOrder& order, const float* gate,
                                   const float* swa_part, void* workspace, int sms, cudaStream_t stream);
 

@@ -424,6 +424,7 @@ static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
     if (kernel == SA_PAGED_TILES) return Choice{true, false, false, false, 0};
     const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
     if (pb.max_new > limit) c = Choice{path != kPathSA, path != kPathSWA, true, false, limit};
+    if (!paged_order_supported(pb)) c.sa_tiles = false;
   }
   // few units of few keys: the unit kernel instead of the row kernel
   if (paged_unit_fits(pb, path, c.row_limit, sms)) {
@@ -501,7 +502,8 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   if (ch.sa_tiles) {
     pb.sa_limit = ch.row_limit;
     SaOrder order;
-    st = launch_paged_order(pb, ch.row_limit, paged_tile_tokens(pb), w + parts.rows + parts.tiles, &order, stream);
+    st = launch_paged_order(pb, ch.row_limit, paged_tile_tokens(pb), w + parts.rows + parts.tiles, &order, ch.tiles,
+                            stream);
     if (st == SA_OK) st = launch_paged_sa_tiles(pb, order, gate_sa, swa_part, w + parts.rows, sms, stream);
     if (st != SA_OK) return st;
   }

@@ -1,17 +1,24 @@
 // A request's tokens in sigma's order, for the SA tiles of the paged-cache
 // attention (sa_paged_tiles.cu).
 //
-// For each request that brings many new tokens, one block passes over its row
-// of sigma and keeps, in order, the entries that name a token there is
-// (sigma[q] < length): the list, with each token's row in the caches.  The new
-// tokens among them are the members; a member at place q has the window
-// |q' - q| <= h, the run of list entries between two binary searches over the
-// places, each within h entries of its own.  Last, the tiles' key chunks are
-// summed, which is what the tile kernel's schedule needs to know.
+// For each request that brings many new tokens, a cluster of eight blocks
+// passes over its row of sigma, an eighth each, and keeps, in order, the entries
+// that name a token there is (sigma[q] < length): the list, with each token's
+// row in the caches.  Beside it stand, for every 32 places of sigma, which of
+// them are in the list and how many are before: rank(q), the list entries at
+// places below q, is then one 8-byte load and a population count.  The new
+// tokens in the list are the members; a member at place q has the window
+// |q' - q| <= h, the list entries rank(q - h) to rank(q + h + 1) - 1.  Last, the
+// tiles' key chunks are summed, which is what the tile kernel's schedule needs.
 //
-// Bound by latency and one SM's loads: perm_len * 4 bytes read, 12 bytes per
-// token written, in rounds of 16384 entries whose order is found by ballots
-// and one scan over the block's 32 warps.
+// Bound by latency, not by its 4 bytes per place read and 8 per token written:
+// sigma, the block table and the ranks one after the other, two cluster
+// barriers, and the launch.  A block holds up to 4096 places of its eighth in
+// registers between the count and the writing; longer rows of sigma are read a
+// second time.  Two requests of 1024 new tokens, 32768 places: 38 us of 180 for
+// the gated call with one block per request, whose members were placed by
+// binary searches; now the call takes 140, with the order found beside the SWA
+// tiles.
 #include "sa_internal.h"
 
 #include <cstring>
@@ -21,7 +28,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kEach = 16;  // entries of sigma per thread and round
+constexpr int kEach = 4;     // places of sigma per thread and round
+constexpr int kCluster = 8;  // blocks per request
 constexpr int kChunk = 128;
 
 struct Params {
@@ -31,6 +39,8 @@ struct Params {
   const int32_t* seq_lens;
   int32_t* err;
   SaOrder order;
+  uint2* words;  // [lists][cap / 32] of each 32 places: which are in the list, entries before them
+  int2* mark;    // [T] members in sigma's order, a request's from q_start on: place, position
   long long perm_stride, page_rows;
   int T, max_new, max_pages, page, num_pages, perm_len, half, row_limit, Bt, Hkv, lists;
 };
@@ -44,107 +54,162 @@ __device__ __forceinline__ int new_tokens(const Params& P, int b, int* len) {
   return ok && paged_sa_tiled(n, *len, P.half, P.row_limit) ? n : 0;
 }
 
-__global__ void __launch_bounds__(kThreads) sa_paged_order_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void cluster_sync() {  // also for what its blocks wrote to memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of block `rank` of the cluster at the place of `p` here.
+__device__ __forceinline__ int2 load_peer(const int2* p, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void order_request(const Params& P) {
   __shared__ int s_a[kWarps], s_b[kWarps];
+  __shared__ int2 s_total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x;
+  const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  int len;
+  int n = new_tokens(P, b, &len);
   // list number: the requests before this one that are taken too
-  int before = 0, len;
-  for (int i = tid; i < b; i += kThreads) before += new_tokens(P, i, &len) > 0;
+  int before = 0, other;
+  for (int i = tid; i < b; i += kThreads) before += new_tokens(P, i, &other) > 0;
   before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) s_a[warp] = before;
   __syncthreads();
   before = __reduce_add_sync(0xffffffffu, s_a[lane]);
-  int n = new_tokens(P, b, &len);
   if (before >= P.lists && n > 0) {  // only where requests claim the same rows
     if (tid == 0) atomicOr(P.err, SA_ERRBIT_RANGE);
     n = 0;
   }
-  if (n == 0) {
-    if (tid == 0) P.order.info[b] = make_int2(before, 0);
+  if (n == 0) {  // (so for every block of the cluster)
+    if (tid == 0 && rank == 0) P.order.info[b] = make_int2(before, 0);
     return;
   }
   const int q0 = P.q_start[b], c = len - n;
   uint2* list = P.order.list + (long long)before * P.order.cap;
-  int32_t* place = P.order.place + (long long)before * P.order.cap;
-  int4* members = P.order.members + q0;
+  uint2* words = P.words + (long long)before * ((P.order.cap + 31) / 32);
+  int2* mark = P.mark + q0;
   const int32_t* sigma = P.perm + (long long)b * P.perm_stride;
   const int32_t* table = P.table + (long long)b * P.max_pages;
   const unsigned below = (1u << lane) - 1u;
-  int entries = 0, found = 0;  // list entries and members so far
-  for (int base = 0; base < P.perm_len; base += kThreads * kEach) {
-    // a warp takes 32 kEach entries that follow each other
-    const int from = base + warp * (32 * kEach) + lane;
-    int tok[kEach];
+  // this block's places, in rounds of kThreads kEach; a warp takes 32 kEach that follow each other
+  const int share = ((P.perm_len - 1) / (kCluster * 32) + 1) * 32;
+  const long long first = (long long)rank * share;
+  const int begin = int(min(first, (long long)P.perm_len));
+  const int end = int(min(first + share, (long long)P.perm_len));
+  int tok[kEach], pg[kEach];
+  auto load = [&](int base, bool report) {  // places `base` + .. of a round
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      const int q = from + 32 * j;
-      tok[j] = q < P.perm_len ? sigma[q] : -1;
-      if (q < P.perm_len && unsigned(tok[j]) >= unsigned(P.perm_len)) {
-        atomicOr(P.err, SA_ERRBIT_RANGE);
+      const long long q = (long long)base + warp * (32 * kEach) + 32 * j + lane;
+      tok[j] = q < end ? sigma[q] : -1;
+      if (q < end && unsigned(tok[j]) >= unsigned(P.perm_len)) {
+        if (report) atomicOr(P.err, SA_ERRBIT_RANGE);
         tok[j] = -1;
       }
       if (tok[j] >= len) tok[j] = -1;
     }
-    int pg[kEach];
-    int count = 0, mine = 0;
+  };
+  auto pages = [&]() {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) pg[j] = tok[j] >= 0 ? table[unsigned(tok[j]) / unsigned(P.page)] : 0;
+  };
+  const bool once = end - begin <= kThreads * kEach;
+  int count = 0, mine = 0;  // this warp's entries and members
+  long long next = begin;
+  do {
+    load(int(next), true);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      pg[j] = tok[j] >= 0 ? table[unsigned(tok[j]) / unsigned(P.page)] : 0;
       count += __popc(__ballot_sync(0xffffffffu, tok[j] >= 0));
       mine += __popc(__ballot_sync(0xffffffffu, tok[j] >= c));
     }
-    __syncthreads();  // the last round's sums are read
-    if (lane == 0) {
-      s_a[warp] = count;
-      s_b[warp] = mine;
+    next += kThreads * kEach;
+  } while (next < end);
+  if (once) pages();
+  __syncthreads();  // s_a has been read
+  if (lane == 0) {
+    s_a[warp] = count;
+    s_b[warp] = mine;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int x = __reduce_add_sync(0xffffffffu, s_a[lane]), y = __reduce_add_sync(0xffffffffu, s_b[lane]);
+    if (lane == 0) s_total = make_int2(x, y);
+  }
+  cluster_sync();
+  const int2 peer = lane < kCluster ? load_peer(&s_total, lane) : make_int2(0, 0);
+  const int entries = __reduce_add_sync(0xffffffffu, peer.x);
+  const int members = __reduce_add_sync(0xffffffffu, peer.y);
+  int at0 = __reduce_add_sync(0xffffffffu, lane < rank ? peer.x : 0);
+  int am0 = __reduce_add_sync(0xffffffffu, lane < rank ? peer.y : 0);
+  next = begin;
+  do {
+    const int base = int(next);
+    if (!once) {
+      load(base, false);
+      pages();
+      count = mine = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        count += __popc(__ballot_sync(0xffffffffu, tok[j] >= 0));
+        mine += __popc(__ballot_sync(0xffffffffu, tok[j] >= c));
+      }
+      __syncthreads();  // the last round's sums are read
+      if (lane == 0) {
+        s_a[warp] = count;
+        s_b[warp] = mine;
+      }
+      __syncthreads();
     }
-    __syncthreads();
     const int ca = s_a[lane], cb = s_b[lane];
-    int at = entries + __reduce_add_sync(0xffffffffu, lane < warp ? ca : 0);
-    int am = found + __reduce_add_sync(0xffffffffu, lane < warp ? cb : 0);
-    entries += __reduce_add_sync(0xffffffffu, ca);
-    found += __reduce_add_sync(0xffffffffu, cb);
+    int at = at0 + __reduce_add_sync(0xffffffffu, lane < warp ? ca : 0);
+    int am = am0 + __reduce_add_sync(0xffffffffu, lane < warp ? cb : 0);
+    at0 += __reduce_add_sync(0xffffffffu, ca);
+    am0 += __reduce_add_sync(0xffffffffu, cb);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
+      const long long q32 = (long long)base + warp * (32 * kEach) + 32 * j;
       const unsigned have = __ballot_sync(0xffffffffu, tok[j] >= 0);
       const unsigned fresh = __ballot_sync(0xffffffffu, tok[j] >= c);
+      if (lane == 0 && q32 < end) words[q32 >> 5] = make_uint2(have, uint32_t(at));
       if (tok[j] >= 0) {
-        const int e = at + __popc(have & below);
         uint32_t row = 0xffffffffu;
         if (unsigned(pg[j]) < unsigned(P.num_pages))
           row = uint32_t(pg[j]) * uint32_t(P.page_rows) +
                 uint32_t(unsigned(tok[j]) % unsigned(P.page)) * uint32_t(P.Hkv);
         else
           atomicOr(P.err, SA_ERRBIT_RANGE);
-        list[e] = make_uint2(row, uint32_t(tok[j]));
-        place[e] = from + 32 * j;
+        list[at + __popc(have & below)] = make_uint2(row, uint32_t(tok[j]));
         const int m = am + __popc(fresh & below);
-        if (tok[j] >= c && m < n) members[m] = make_int4(e, from + 32 * j, 0, tok[j]);
+        if (tok[j] >= c && m < n) mark[m] = make_int2(int(q32) + lane, tok[j]);
       }
       at += __popc(have);
       am += __popc(fresh);
     }
-  }
+    next += kThreads * kEach;
+  } while (next < end);
   // sigma names each token once, else the rows of some are left as they were
-  if (found != n && tid == 0) atomicOr(P.err, SA_ERRBIT_RANGE);
-  found = min(found, n);
-  __syncthreads();
-  for (int m = tid; m < found; m += kThreads) {
-    const int4 x = members[m];
-    int lo = max(0, x.x - P.half), hi = x.x;  // first entry with place >= q - h
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (place[mid] >= x.y - P.half) hi = mid; else lo = mid + 1;
-    }
-    int lo2 = x.x, hi2 = int(min((long long)entries - 1, (long long)x.x + P.half));  // last with place <= q + h
-    while (lo2 < hi2) {
-      const int mid = (lo2 + hi2 + 1) >> 1;
-      if ((long long)place[mid] <= (long long)x.y + P.half) lo2 = mid; else hi2 = mid - 1;
-    }
-    members[m] = make_int4(lo, lo2, q0 + x.w - c, x.w);
+  if (members != n && tid == 0 && rank == 0) atomicOr(P.err, SA_ERRBIT_RANGE);
+  const int found = min(members, n);
+  cluster_sync();  // (also: nobody exits before its s_total is read)
+  auto entries_below = [&](long long q) {
+    if (q >= P.perm_len) return entries;
+    const uint2 w = words[q >> 5];
+    return int(w.y) + __popc(w.x & ((1u << (q & 31)) - 1u));
+  };
+  auto window_first = [&](int q) { return entries_below(max(0, q - P.half)); };
+  auto window_last = [&](int q) { return entries_below((long long)q + P.half + 1) - 1; };
+  for (int m = rank * kThreads + tid; m < found; m += kCluster * kThreads) {
+    const int2 x = mark[m];
+    P.order.members[q0 + m] = make_int4(window_first(x.x), window_last(x.x), q0 + x.y - c, x.y);
   }
-  __syncthreads();
+  if (rank != kCluster - 1) return;
   // the tiles' chunks, summed
   int32_t* chunks = P.order.chunks + q0 + b;
   const int tiles = (found + P.Bt - 1) / P.Bt;
@@ -153,8 +218,8 @@ __global__ void __launch_bounds__(kThreads) sa_paged_order_kernel(const __grid_c
     const int g = g0 + tid;
     int x = 0;
     if (g < tiles) {
-      const int first = g * P.Bt, last = min(found, first + P.Bt) - 1;
-      x = (members[last].y + 1 - members[first].x + kChunk - 1) / kChunk;
+      const int m0 = g * P.Bt, m1 = min(found, m0 + P.Bt) - 1;
+      x = (window_last(mark[m1].x) - window_first(mark[m0].x) + kChunk) / kChunk;
     }
     int in = x;
 #pragma unroll
@@ -176,36 +241,49 @@ __global__ void __launch_bounds__(kThreads) sa_paged_order_kernel(const __grid_c
   }
 }
 
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    sa_paged_order_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  order_request(P);
+  // Launched beside the SWA tiles, of whose results it needs none; but whoever
+  // waits for this kernel waits for them too.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The most requests that can be taken: each has more than row_limit tokens.
 long long lists(const PagedProblem& pb, int row_limit) {
   return min((long long)pb.B, (long long)pb.T / (row_limit + 1LL));
 }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+size_t word_bytes(const PagedProblem& pb, int row_limit) {
+  return round256(size_t(lists(pb, row_limit)) * ((size_t(pb.perm_len) + 31) / 32) * 8);
+}
 
 }  // namespace
 
 size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit) {
   const size_t n = size_t(lists(pb, row_limit)) * size_t(pb.perm_len);
-  return round256(n * 8) + round256(n * 4) + round256(size_t(pb.T) * 16) +
+  return round256(n * 8) + word_bytes(pb, row_limit) + round256(size_t(pb.T) * 24) +
          round256((size_t(pb.T) + size_t(pb.B)) * 4) + round256(size_t(pb.B) * 8);
 }
 
 sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_tokens, void* workspace,
-                               SaOrder* order, cudaStream_t stream) {
+                               SaOrder* order, bool beside, cudaStream_t stream) {
   const size_t n = size_t(lists(pb, row_limit)) * size_t(pb.perm_len);
   char* w = static_cast<char*>(workspace);
   order->list = reinterpret_cast<uint2*>(w);
   w += round256(n * 8);
-  order->place = reinterpret_cast<int32_t*>(w);
-  w += round256(n * 4);
+  Params P;
+  std::memset(&P, 0, sizeof(P));
+  P.words = reinterpret_cast<uint2*>(w);
+  w += word_bytes(pb, row_limit);
   order->members = reinterpret_cast<int4*>(w);
-  w += round256(size_t(pb.T) * 16);
+  P.mark = reinterpret_cast<int2*>(w + size_t(pb.T) * 16);
+  w += round256(size_t(pb.T) * 24);
   order->chunks = reinterpret_cast<int32_t*>(w);
   w += round256((size_t(pb.T) + size_t(pb.B)) * 4);
   order->info = reinterpret_cast<int2*>(w);
   order->cap = pb.perm_len;
-  Params P;
-  std::memset(&P, 0, sizeof(P));
   P.perm = pb.perm;
   P.table = pb.table;
   P.q_start = pb.q_start;
@@ -225,8 +303,16 @@ sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_t
   P.Bt = tile_tokens;
   P.Hkv = pb.Hkv;
   P.lists = int(lists(pb, row_limit));
-  sa_paged_order_kernel<<<unsigned(pb.B), kThreads, 0, stream>>>(P);
-  const cudaError_t ce = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(pb.B) * kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = beside ? 1 : 0;
+  const cudaError_t ce = cudaLaunchKernelEx(&cfg, sa_paged_order_kernel, P);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged order launch: %s", cudaGetErrorString(ce));
   return SA_OK;
 }
