@@ -21,13 +21,13 @@
 //
 // Measured (2048 new tokens at the end of 32768, every key in the window, 32 q
 // heads on 8 kv heads, d = 128: 1.06 PFLOP; 568 us at cuBLAS's burst rate):
-//   one MMA warp, softmax over 128 columns at once         857-880 us
+//   one MMA warp, softmax over 128 columns at once         857-880 us (one producer)
 //   64-key parts, two MMA warps, softmax loop unrolled         935 us
-//   the same, the loop over the parts not unrolled         854-875 us
+//   the same, the loop over the parts not unrolled         854-875 us, two producers 797-834
 //   S of all 128 keys by one MMA of N = 128, P in parts        937 us
 //   the halves taking turns, 16 softmax warps in pairs         882 us
 // The unrolled softmax loop does not fit the instruction cache beside the
-// other roles' code.  What is left between 855 and the tensor cores' time is
+// other roles' code.  What is left between 817 and the tensor cores' time is
 // the chain S -> softmax -> P V -> S of a part (1900 cycles, of which 640 are
 // the MMAs of one half).
 //
@@ -48,10 +48,15 @@
 // it starts in.
 //
 // Roles (12 warps):
-//   warp 0      producer: TMA.  A lane takes a page of the chunk and loads its
-//               run of rows in boxes of 64, 16, 4 and 1 rows of 128 bytes; lane
-//               0 loads a tile's Q as one box per 64 columns.  (SA: warps 0 and
-//               3, cp.async)
+//   warps 0, 3  producers, of Q and K and of V: TMA.  A lane takes a page of the
+//               chunk and loads its run of rows in two boxes of 128-byte rows,
+//               the largest power of two in the run from its start and as many
+//               rows up to its end, which may overlap.  (One warp for both, with
+//               boxes of 64, 16, 4 and 1 rows, nine rounds of them for a ragged
+//               run, took 5400 cycles a chunk where pages of 48 tokens end
+//               anywhere: 78.5 us for the mixed batch against 58, and 857
+//               against 817 for the long prompt.)
+//               SA: rows from anywhere by cp.async
 //   warps 1, 2  the elected lane issues the MMAs of half 0, of half 1; warp 1
 //               owns TMEM
 //   warps 4-11  softmax and epilogue: warp 4 + 4 h + i takes rows 32 i .. of
@@ -81,6 +86,7 @@ constexpr int kKC = 128;            // keys per chunk: of one load
 constexpr int kSub = 64;            // keys per part of a chunk: of one softmax step
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kCutChunks = 32;      // tiles this long on average may be cut
+constexpr int kBoxes = 7;           // boxes of up to 64 rows
 constexpr uint32_t kMaxSmem = 232448;
 
 struct Desc {  // per block: the tile that starts in its run and ends beyond it
@@ -89,7 +95,7 @@ struct Desc {  // per block: the tile that starts in its run and ends beyond it
 
 struct Params {
   CUtensorMap tq;           // q [T, Hq, D] in boxes of a tile's rows
-  CUtensorMap tk[4], tv[4]; // caches [pages, page, Hkv, D] in boxes of 4^i rows of a page
+  CUtensorMap tk[kBoxes], tv[kBoxes]; // caches [pages, page, Hkv, D] in boxes of 2^i rows of a page
   const int32_t* table;
   const int32_t* q_start;
   const int32_t* seq_lens;
@@ -207,17 +213,19 @@ __device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap* tm, in
 // sum_{i=0}^{n-1} floor((a i + b) / m), a, b >= 0: lattice points under a line,
 // counted by Euclid's descent -- take out the integer parts of slope and
 // offset, then exchange the axes.
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// (a n + b fits 32 bits: 64-bit divisions take several times as long, and a
+// block does nothing else until its run is found.)
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long s = 0;
   while (n > 0) {
-    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    s += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
     a %= m;
     b %= m;
-    const long long top = a * n + b;
+    const uint32_t top = a * n + b;
     if (top < m) break;
     n = top / m;
     b = top % m;
-    const long long t = a;
+    const uint32_t t = a;
     a = m;
     m = t;
   }
@@ -282,12 +290,12 @@ __device__ __forceinline__ long long chunks_before(const Params& P, const Reques
     --k;
     s = tile_chunks<SA>(P, r, k);
   }
-  // tiles whose window reaches the first key: hi = c + (i + 1) Bt keys
-  const long long c = r.len - r.n;
-  const long long reach = (long long)P.w - 1 - c;  // largest first-token offset with lo = 0
-  long long ka = reach < 0 ? 0 : reach / P.Bt + 1;
-  if (ka > k) ka = k;
-  s += floor_sum(ka, kKC, P.Bt, c + P.Bt + kKC - 1);
+  // tiles whose window reaches the first key: hi = c + (i + 1) Bt keys, at most
+  // the request's length (a full tile ends there or before)
+  const int c = r.len - r.n;
+  const int reach = P.w - 1 - c;  // largest first-token offset with lo = 0
+  const int ka = reach < 0 ? 0 : min(reach / P.Bt + 1, k);
+  s += floor_sum(uint32_t(ka), kKC, uint32_t(P.Bt), uint32_t(c) + uint32_t(P.Bt + kKC - 1));
   s += (k - ka) * (((long long)P.Bt + P.w - 1 + kKC - 1) / kKC);
   return s;
 }
@@ -483,39 +491,46 @@ struct KeysOf { using T = Keys; };
 template <>
 struct KeysOf<true> { using T = SaKeys; };
 
-// A run of `len` rows of a page from row `in` to rows r .. of a stage, in
-// boxes of 64, 16, 4 and 1 rows; or `len` copies of one row.
+// Rows that load_run moves for a run of `len` rows, 1 <= len <= 128.
+__device__ __forceinline__ int run_rows(int len) {
+  const int step = 1 << min(kBoxes - 1, 31 - __clz(len));
+  return len == step ? step : 2 * step;
+}
+// A run of `len` rows of a page from row `in` to rows r .. of a stage: a box of
+// 2^i <= len rows from its start and one up to its end, which may overlap.
 template <int D>
 __device__ __forceinline__ void load_run(const CUtensorMap* maps, uint32_t dst, int r, int len, int in,
-                                         int page, int kvh, bool same, uint32_t bar) {
+                                         int page, int kvh, uint32_t bar) {
+  const int i = min(kBoxes - 1, 31 - __clz(len)), rest = len - (1 << i);
 #pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    const int step = 1 << (2 * i);
-    if (same && i > 0) continue;
-    for (; len >= step; len -= step) {
+  for (int kb = 0; kb < D / 64; ++kb)
+    tma_box4(dst + uint32_t(kb * (kKC * 128) + r * 128), maps + i, kb * 64, kvh, in, page, bar);
+  if (rest > 0) {
 #pragma unroll
-      for (int kb = 0; kb < D / 64; ++kb)
-        tma_box4(dst + uint32_t(kb * (kKC * 128) + r * 128), maps + i, kb * 64, kvh, in, page, bar);
-      r += step;
-      if (!same) in += step;
-    }
+    for (int kb = 0; kb < D / 64; ++kb)
+      tma_box4(dst + uint32_t(kb * (kKC * 128) + (r + rest) * 128), maps + i, kb * 64, kvh, in + rest, page, bar);
   }
 }
 
+// Warp 0 brings Q, K and what the other roles need to know, warp 3 brings V.
 template <int D, int NS>
 __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
                               uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
   const int lane = threadIdx.x & 31;
+  const bool is_v = threadIdx.x >= 32;
+  const uint32_t full = is_v ? BR::kVfull : BR::kKfull, free = is_v ? BR::kVfree : BR::kKfree;
+  const CUtensorMap* maps = is_v ? P.tv : P.tk;
+  const uint32_t stages = sbase + (is_v ? P.off_v : P.off_k);
   auto wwait = [&](uint32_t bar, uint32_t parity) {
     const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
     return __all_sync(0xffffffffu, ok);
   };
   Cursor cur = make_cursor<false>(P, start);
   Seg s, ahead;
-  int n = 0, x = 0;             // chunks and tiles so far
-  int nq = 0, nk = 0, nv = 0;   // Q, K and V loads begun
+  int n = 0, x = 0;    // chunks and tiles so far
+  int nq = 0, nk = 0;  // Q loads and loads of this warp's stages begun
   bool ok = true;
   bool more = next_seg<false>(P, cur, ahead);
   for (; ok && more; ++x) {
@@ -528,33 +543,35 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
     const int last_col = int(unsigned(hi - 1) / unsigned(P.page));
     auto page_at = [&](int col) { return col <= last_col ? table[col] : -1; };
     int page = page_at(int(unsigned(lo + s.c0 * kKC) / unsigned(P.page)) + lane);
-    if (x > 3 && !(ok = wwait(BR::kSegFree + (x & 3), uint32_t((x >> 2) - 1)))) break;
-    if (lane == 0) {
-      Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
-      sh->t0 = s.r.q0 + i0;
-      sh->nt = min(P.Bt, s.r.n - i0);
-      sh->pos0 = s.r.len - s.r.n + i0;
-      sh->lo = lo;
-      sh->kvh = s.kvh;
-      sh->c0 = s.c0;
-      sh->c1 = s.c1;
-      sh->nch = s.nch;
-      sh->a[0] = sh->a[1] = sh->b[1] = s.c0;
-      sh->b[0] = s.c1;
-      if (min(P.Bt, s.r.n - i0) * P.g > kBM) sh->b[1] = s.c1;  // else half 1 has no rows
-      sh->more = more;
-      // a run that ends inside a tile is a full one
-      sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
-      mbar_arrive(bars + 8 * (BR::kSegFull + (x & 3)));
+    if (!is_v) {
+      if (x > 3 && !(ok = wwait(BR::kSegFree + (x & 3), uint32_t((x >> 2) - 1)))) break;
+      if (lane == 0) {
+        Shared* sh = reinterpret_cast<Shared*>(smem + P.off_seg) + (x & 3);
+        sh->t0 = s.r.q0 + i0;
+        sh->nt = min(P.Bt, s.r.n - i0);
+        sh->pos0 = s.r.len - s.r.n + i0;
+        sh->lo = lo;
+        sh->kvh = s.kvh;
+        sh->c0 = s.c0;
+        sh->c1 = s.c1;
+        sh->nch = s.nch;
+        sh->a[0] = sh->a[1] = sh->b[1] = s.c0;
+        sh->b[0] = s.c1;
+        if (min(P.Bt, s.r.n - i0) * P.g > kBM) sh->b[1] = s.c1;  // else half 1 has no rows
+        sh->more = more;
+        // a run that ends inside a tile is a full one
+        sh->join = s.c1 < s.nch && s.c0 == 0 ? int((s.pos + s.nch - 1) / (start.end - start.begin)) : -1;
+        mbar_arrive(bars + 8 * (BR::kSegFull + (x & 3)));
+      }
+      if (x > 0 && !(ok = wwait(BR::kQfree, uint32_t(x - 1)))) break;
+      if (lane == 0) {
+        // rows of other tokens behind the tile's are computed and not written
+        mbar_arrive_expect_tx(bars + 8 * BR::kQfull, uint32_t(P.Bt * P.g) * D * 2);
+        for (int kb = 0; kb < D / 64; ++kb)
+          tma_box3(sbase + kb * (kRows * 128), &P.tq, kb * 64, s.kvh * P.g, s.r.q0 + i0, bars + 8 * BR::kQfull);
+      }
+      ++nq;
     }
-    if (x > 0 && !(ok = wwait(BR::kQfree, uint32_t(x - 1)))) break;
-    if (lane == 0) {
-      // rows of other tokens behind the tile's are computed and not written
-      mbar_arrive_expect_tx(bars + 8 * BR::kQfull, uint32_t(P.Bt * P.g) * D * 2);
-      for (int kb = 0; kb < D / 64; ++kb)
-        tma_box3(sbase + kb * (kRows * 128), &P.tq, kb * 64, s.kvh * P.g, s.r.q0 + i0, bars + 8 * BR::kQfull);
-    }
-    ++nq;
     // a good key's place, which stands in for keys of bad pages (whose weight is 0)
     int gpage = 0, gin = 0;
     bool good = false;
@@ -562,6 +579,7 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       const int st = n % NS;
       const int j0 = lo + c * kKC, j1 = min(hi, j0 + kKC);
       const int col0 = int(unsigned(j0) / unsigned(P.page)), cols = int(unsigned(j1 - 1) / unsigned(P.page)) - col0 + 1;
+      const int steps = (j1 - j0 + 15) / 16, fill = steps * 16 - (j1 - j0);
       // this lane's run of keys: those of table column col0 + i
       auto run = [&](int i, int& r, int& len, int& in) {
         const int a = max(j0, (col0 + i) * P.page);
@@ -573,20 +591,23 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       uint32_t bad[4] = {0, 0, 0, 0};
       bool any_bad = false;
       int last_good = -1;
+      int rows = 0;  // that this lane's copies bring
       for (int i = lane; i < cols; i += 32) {
         const int pg = i < 32 ? page : table[col0 + i];
+        int r, len, in;
+        run(i, r, len, in);
         if (unsigned(pg) < unsigned(P.num_pages)) {
           last_good = i;
+          rows += run_rows(len);
         } else {
-          int r, len, in;
-          run(i, r, len, in);
 #pragma unroll
           for (int w = 0; w < 4; ++w) bad[w] |= band_bits(r, r + len - 1, w * 32);
           any_bad = true;
+          rows += len;
         }
       }
+      rows = __reduce_add_sync(0xffffffffu, rows);
       const unsigned fine = __ballot_sync(0xffffffffu, last_good >= 0);
-      uint32_t words = 0;  // lanes 0-3: the chunk's bad keys
       if (fine != 0u) {
         const int src = 31 - __clz(int(fine));
         const int i = __shfl_sync(0xffffffffu, last_good, src);
@@ -595,49 +616,43 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
         gpage = i < 32 ? __shfl_sync(0xffffffffu, page, i) : table[col0 + i];
         good = true;
       }
-      if (__any_sync(0xffffffffu, any_bad)) {
-        if (any_bad) atomicOr(P.err, SA_ERRBIT_RANGE);
+      if (!is_v) {
+        uint32_t words = 0;  // lanes 0-3: the chunk's bad keys
+        if (__any_sync(0xffffffffu, any_bad)) {
+          if (any_bad) atomicOr(P.err, SA_ERRBIT_RANGE);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t v = __reduce_or_sync(0xffffffffu, bad[w]);
-          if (lane == w) words = v;
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t v = __reduce_or_sync(0xffffffffu, bad[w]);
+            if (lane == w) words = v;
+          }
+        }
+        Keys* keys = reinterpret_cast<Keys*>(smem + P.off_bad) + (n % kKeySlots);
+        if (lane < 4) keys->bad[lane] = words;
+        if (lane == 0) {
+          keys->good = good;
+          keys->steps = steps;
         }
       }
-      Keys* keys = reinterpret_cast<Keys*>(smem + P.off_bad) + (n % kKeySlots);
-      const int steps = (j1 - j0 + 15) / 16, fill = steps * 16 - (j1 - j0);
-      if (lane < 4) keys->bad[lane] = words;
-      if (lane == 0) {
-        keys->good = good;
-        keys->steps = steps;
-      }
-      auto load = [&](const CUtensorMap* maps, uint32_t dst, uint32_t bar) {
-        for (int i = lane; i < cols; i += 32) {
-          const int pg = i < 32 ? page : table[col0 + i];
-          const bool ok_page = unsigned(pg) < unsigned(P.num_pages);
-          int r, len, in;
-          run(i, r, len, in);
-          load_run<D>(maps, dst, r, len, ok_page ? in : gin, ok_page ? pg : gpage, s.kvh, !ok_page, bar);
+      if (n >= NS && !(ok = wwait(free + st, uint32_t(n / NS - 1)))) break;
+      __syncwarp();
+      // K rows past the last key keep what they held: their scores are masked.
+      // The last step's V rows past it are copies of a real row, since weights of
+      // 0 times what happens to be there need not be 0.
+      const uint32_t bar = bars + 8 * (full + st), dst = stages + uint32_t(st) * kTile;
+      if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(rows + (is_v ? fill : 0)) * D * 2);
+      __syncwarp();
+      for (int i = lane; i < cols; i += 32) {
+        const int pg = i < 32 ? page : table[col0 + i];
+        int r, len, in;
+        run(i, r, len, in);
+        if (unsigned(pg) < unsigned(P.num_pages)) {
+          load_run<D>(maps, dst, r, len, in, pg, s.kvh, bar);
+        } else {
+          for (int e = 0; e < len; ++e) load_run<D>(maps, dst, r + e, 1, gin, gpage, s.kvh, bar);
         }
-      };
-      if (n >= NS && !(ok = wwait(BR::kKfree + st, uint32_t(n / NS - 1)))) break;
-      __syncwarp();
-      if (lane == 0)
-        mbar_arrive_expect_tx(bars + 8 * (BR::kKfull + st), uint32_t(j1 - j0) * D * 2);
-      __syncwarp();
-      // K rows past the last key keep what they held: their scores are masked
-      load(P.tk, sbase + P.off_k + uint32_t(st) * kTile, bars + 8 * (BR::kKfull + st));
+      }
+      if (is_v && lane < fill) load_run<D>(maps, dst, j1 - j0 + lane, 1, gin, gpage, s.kvh, bar);
       ++nk;
-      if (n >= NS && !(ok = wwait(BR::kVfree + st, uint32_t(n / NS - 1)))) break;
-      if (lane == 0)
-        mbar_arrive_expect_tx(bars + 8 * (BR::kVfull + st), uint32_t(steps * 16) * D * 2);
-      __syncwarp();
-      load(P.tv, sbase + P.off_v + uint32_t(st) * kTile, bars + 8 * (BR::kVfull + st));
-      // the last step's V rows past the last key: copies of a real row, since
-      // weights of 0 times what happens to be there need not be 0
-      if (lane < fill)
-        load_run<D>(P.tv, sbase + P.off_v + uint32_t(st) * kTile, j1 - j0 + lane, 1, gin, gpage, s.kvh, true,
-                    bars + 8 * (BR::kVfull + st));
-      ++nv;
       if (c + 1 < s.c1) page = page_at(int(unsigned(j0 + kKC) / unsigned(P.page)) + lane);
     }
   }
@@ -651,10 +666,7 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       }
     };
     drain(BR::kQfull, nq);
-    for (int i = 0; i < NS; ++i) {
-      drain(BR::kKfull + i, nk > i ? (nk - i + NS - 1) / NS : 0);
-      drain(BR::kVfull + i, nv > i ? (nv - i + NS - 1) / NS : 0);
-    }
+    for (int i = 0; i < NS; ++i) drain(full + i, nk > i ? (nk - i + NS - 1) / NS : 0);
   }
   __syncwarp();
 }
@@ -1239,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
     mma_role<D, NS, SA>(P, warp - kMmaWarp, any, seg, keys, sbase, tmem, bars, abort_flag);
   } else if (SA) {
     sa_producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, s_vote);
-  } else if (warp == 0) {
+  } else {
     producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag);
   }
   tc_fence_before();
@@ -1414,8 +1426,8 @@ sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const floa
   bool maps = encode_box_map(&P.tq, pb.q, 3, qdims, qst, qbox);
   const uint64_t dims[4] = {uint64_t(pb.d), uint64_t(pb.Hkv), uint64_t(pb.page), uint64_t(pb.num_pages)};
   const uint64_t st[3] = {d2, d2 * pb.Hkv, uint64_t(pb.page_stride) * 2};
-  for (int i = 0; i < 4 && maps; ++i) {
-    const uint32_t box[4] = {64, 1, 1u << (2 * i), 1};
+  for (int i = 0; i < kBoxes && maps && 1 << i <= pb.page; ++i) {  // (no longer runs in a page)
+    const uint32_t box[4] = {64, 1, 1u << i, 1};
     maps = encode_box_map(&P.tk[i], pb.k, 4, dims, st, box) && encode_box_map(&P.tv[i], pb.v, 4, dims, st, box);
   }
   if (!maps) return fail(SA_ERR_CUDA, "paged tile kernel: cannot encode the tensor maps");
