@@ -144,6 +144,32 @@ cudaError_t allow_smem(uint32_t bytes) {
   return ce;
 }
 
+// Launches a kernel; `beside`: it may start while the kernel before it in the
+// stream still runs (once each block of that one allows it or has ended), and
+// orders itself with griddepcontrol.wait.
+template <class P>
+cudaError_t launch_kernel(void (*kernel)(P), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t stream,
+                          bool beside, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+#ifdef __CUDACC__
+// The end of a kernel that needs nothing of the one that it runs beside: its
+// last block outlasts that one, so who waits for this kernel waits for both.
+__device__ __forceinline__ void end_beside() {
+  if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
 // Attention over a paged cache, already validated on the host.
 struct PagedProblem {
   int B, T, max_new, Hq, Hkv, d, g;
@@ -165,6 +191,7 @@ struct PagedProblem {
   const float* gate_swa;
   void* out;
   int32_t* err;
+  bool beside;               // the row or unit kernel runs beside the tile kernel
   int sa_limit;              // requests with more new tokens may go to the SA tiles (paged_sa_tiled)
 };
 

@@ -507,6 +507,7 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
     if (st == SA_OK) st = launch_paged_sa_tiles(pb, order, gate_sa, swa_part, w + parts.rows, sms, stream);
     if (st != SA_OK) return st;
   }
+  pb.beside = (ch.tiles || ch.sa_tiles) && path != kPathGated;  // (gated: it adds the SWA tiles' part)
   if (ch.unit) {
     st = launch_paged_unit(pb, path, ch.row_limit, swa_part, stream);
     if (st != SA_OK) return st;

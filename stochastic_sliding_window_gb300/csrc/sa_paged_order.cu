@@ -245,9 +245,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     sa_paged_order_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   order_request(P);
-  // Launched beside the SWA tiles, of whose results it needs none; but whoever
-  // waits for this kernel waits for them too.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  end_beside();  // (the SWA tiles)
 }
 
 // The most requests that can be taken: each has more than row_limit tokens.
@@ -303,16 +301,8 @@ sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_t
   P.Bt = tile_tokens;
   P.Hkv = pb.Hkv;
   P.lists = int(lists(pb, row_limit));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(pb.B) * kCluster);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = beside ? 1 : 0;
-  const cudaError_t ce = cudaLaunchKernelEx(&cfg, sa_paged_order_kernel, P);
+  const cudaError_t ce =
+      launch_kernel(sa_paged_order_kernel, dim3(unsigned(pb.B) * kCluster), kThreads, 0, stream, beside, P);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged order launch: %s", cudaGetErrorString(ce));
   return SA_OK;
 }

@@ -124,15 +124,12 @@ __host__ __device__ constexpr int most_warps(int d, int nt) {
 }
 
 template <int D, int PATH, int NT>
-__global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
-    sa_paged_rows_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void rows_role(const Params& P) {
   constexpr int kPitch = Pitch<D>;
   constexpr int kCpr = D / 8;  // 16-byte chunks per row
   constexpr uint32_t kOffQ = 2 * kKeys * kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  // the join kernel's blocks may be put on SMs that this grid has left
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int worker = warp * int(gridDim.x) + int(blockIdx.x);
   uint8_t* ring = smem_raw + size_t(warp) * P.warp_bytes;
   const uint32_t sring = smem_u32(ring);
@@ -446,6 +443,15 @@ __global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+template <int D, int PATH, int NT>
+__global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
+    sa_paged_rows_kernel(const __grid_constant__ Params P) {
+  // the join kernel's blocks may be put on SMs that this grid has left
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  rows_role<D, PATH, NT>(P);
+  end_beside();
+}
+
 // Joins the parts of each unit that the runs cut, piece after piece in worker
 // order: block c takes the unit that starts in worker c's run.
 template <int D, int PATH>
@@ -538,8 +544,8 @@ static cudaError_t launch_rows(const Params& P, const Config& c, int sms, cudaSt
   const uint32_t smem = c.warp_bytes * uint32_t(c.warps);
   const cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH, NT>>(kMaxSmem);
   if (ce != cudaSuccess) return ce;
-  sa_paged_rows_kernel<D, PATH, NT><<<sms, 32 * c.warps, smem, stream>>>(P);
-  return cudaGetLastError();
+  return launch_kernel(sa_paged_rows_kernel<D, PATH, NT>, dim3(unsigned(sms)), unsigned(32 * c.warps), smem, stream,
+                       P.beside, P);
 }
 
 template <int D, int PATH>
@@ -547,16 +553,7 @@ static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStr
   const cudaError_t ce = c.R <= 8 ? launch_rows<D, PATH, 1>(P, c, sms, stream) : launch_rows<D, PATH, 2>(P, c, sms, stream);
   if (ce != cudaSuccess || c.snap) return ce;
   // its blocks may be set up while the row kernel's last ones finish
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(c.workers));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sa_paged_join_kernel<D, PATH>, P);
+  return launch_kernel(sa_paged_join_kernel<D, PATH>, dim3(unsigned(c.workers)), 128, 0, stream, true, P);
 }
 
 void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, const float* swa_part) {
@@ -586,6 +583,7 @@ void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, 
   P.max_new = pb.max_new;
   P.row_limit = row_limit;
   P.sa_limit = pb.sa_limit;
+  P.beside = pb.beside;
   P.Hq = pb.Hq;
   P.Hkv = pb.Hkv;
   P.g = pb.g;

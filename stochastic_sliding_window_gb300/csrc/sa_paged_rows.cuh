@@ -44,6 +44,7 @@ struct Params {
   int slot_floats;        // one partial: O [R, D], then (m, l) [R]; a multiple of 4
   int workers, min_tiles, snap;  // snap: runs end at unit ends
   uint32_t stage_bytes, warp_bytes;
+  int beside;             // launched beside the tile kernel
   int gmax, list_keys, stages;    // unit kernel: groups per request, key list, stages per warp
   float scale_log2;
 };

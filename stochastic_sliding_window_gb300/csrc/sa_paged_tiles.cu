@@ -46,8 +46,10 @@
 // run may end inside a tile: both parts leave fp32 partials in the workspace
 // and the join kernel merges them in order.  Else a tile belongs to the run
 // it starts in.
+// Measured with tiles cut from 8 chunks on instead: a mixed batch of 9 chunks a
+// tile 56 us instead of 43, a gated chunk 115 instead of 114.
 //
-// Roles (12 warps):
+// Roles (12 warps, SA 14):
 //   warps 0, 3  producers, of Q and K and of V: TMA.  A lane takes a page of the
 //               chunk and loads its run of rows in two boxes of 128-byte rows,
 //               the largest power of two in the run from its start and as many
@@ -56,7 +58,7 @@
 //               run, took 5400 cycles a chunk where pages of 48 tokens end
 //               anywhere: 78.5 us for the mixed batch against 58, and 857
 //               against 817 for the long prompt.)
-//               SA: rows from anywhere by cp.async
+//               SA: warps 0, 3, 12 and 13, rows from anywhere by cp.async
 //   warps 1, 2  the elected lane issues the MMAs of half 0, of half 1; warp 1
 //               owns TMEM
 //   warps 4-11  softmax and epilogue: warp 4 + 4 h + i takes rows 32 i .. of
@@ -79,6 +81,7 @@ namespace ptile {
 using namespace tcc;
 
 constexpr int kThreads = 384;
+constexpr int kSaThreads = 448;     // SA: two more producers
 constexpr int kMmaWarp = 1;
 constexpr int kFirstSoftmaxWarp = 4;
 constexpr int kRows = 2 * kBM;
@@ -671,9 +674,12 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
   __syncwarp();
 }
 
-// SA: rows from anywhere, so cp.async by two warps.  The list's entries of a
-// chunk are read one chunk ahead, two keys a thread.
-constexpr int kSaProducers = 64;
+// SA: rows from anywhere, so cp.async by four warps.  The list's entries of a
+// chunk are read one chunk ahead, one key a thread.  (A warp issues one cp.async
+// in 80 cycles here: two warps made 140 us of a gated call that takes 129 with
+// four, and 131 with six.)
+constexpr int kSaProducers = 128;
+static_assert(kSaProducers == kKC, "a key a thread");
 
 template <int D, int NS>
 __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
@@ -683,7 +689,8 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
   constexpr int CPR = D / 8;               // 16-byte chunks per row
   constexpr int RPP = kSaProducers / CPR;  // rows per pass
   const int lane = threadIdx.x & 31;
-  const int tid = threadIdx.x < 32 ? int(threadIdx.x) : int(threadIdx.x) - 64;  // warps 0 and 3
+  // warps 0, 3, 12 and 13
+  const int tid = int(threadIdx.x) - (threadIdx.x < 32 ? 0 : threadIdx.x < 128 ? 64 : 320);
   const int cc = tid % CPR, r_first = tid / CPR;
   const uint32_t col = uint32_t(cc >> 3) * (kKC * 128), c8 = uint32_t(cc & 7);
   uint32_t* srow = reinterpret_cast<uint32_t*>(smem + P.off_seg + 4 * sizeof(Shared));  // [2][128]
@@ -738,7 +745,7 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
       const int j = lo + c * kKC + at;
       return j < hi ? list[j] : make_uint2(0xffffffffu, 0x7fffffffu);
     };
-    uint2 e0 = entry(s.c0, tid), e1 = entry(s.c0, kSaProducers + tid);
+    uint2 e = entry(s.c0, tid);
     const bool entry_used = x > 3;
     if (tid == 0) {
       // each half's chunks: from its first member's window to its last one's
@@ -799,27 +806,22 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
       const int st = n % NS;
       SaKeys* keys = reinterpret_cast<SaKeys*>(smem + P.off_bad) + (n % kKeySlots);
       uint32_t* rows = srow + (n & 1) * kKC;
-      auto put = [&](int at, uint2 e) {
-        const int j = lo + c * kKC + at;
+      {
+        const int j = lo + c * kKC + tid;
         const uint32_t bad = __ballot_sync(0xffffffffu, j < hi && e.x == 0xffffffffu);
         const uint32_t fresh = __ballot_sync(0xffffffffu, j < hi && int(e.y) >= first_new);
-        rows[at] = e.x == 0xffffffffu ? e.x : e.x + uint32_t(s.kvh);
-        keys->toks[at] = int(e.y);
+        rows[tid] = e.x == 0xffffffffu ? e.x : e.x + uint32_t(s.kvh);
+        keys->toks[tid] = int(e.y);
         if (lane == 0) {
-          keys->bad[at >> 5] = bad;
-          keys->fresh[at >> 5] = fresh;
+          keys->bad[tid >> 5] = bad;
+          keys->fresh[tid >> 5] = fresh;
         }
-      };
-      put(tid, e0);
-      put(kSaProducers + tid, e1);
+      }
       if (tid == 0) {
         keys->good = 1;  // rows that are not there are zeros
         keys->steps = kKC / 16;
       }
-      if (c + 1 < s.c1) {
-        e0 = entry(c + 1, tid);
-        e1 = entry(c + 1, kSaProducers + tid);
-      }
+      if (c + 1 < s.c1) e = entry(c + 1, tid);
       if (!(ok = agree(BR::kKfree + st, uint32_t(n / NS - 1), n >= NS))) break;
       rows_in(kbase, sbase + P.off_k + uint32_t(st) * kTile + col, rows);
       cp_async_arrive_noinc(bars + 8 * (BR::kKfull + st));
@@ -997,6 +999,23 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
         if (u >= parts) break;
         if (!wait(BR::kSfull + 2 * h + u, uint32_t(k[u]))) return;
         tc_fence_after();
+        if constexpr (SA) {  // the warp's rows have no keys here: most of its tile's parts
+          const int at = c * kKC + u * kSub;
+          if (__all_sync(0xffffffffu, khi < at || klo >= at + kSub)) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+            tmem_st16(sb + u * kSub, zero);
+            tmem_st16(sb + u * kSub + 16, zero);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (BR::kPfull + 2 * h + u));
+            ++k[u];
+            last_u = u;
+            continue;
+          }
+        }
         uint32_t v[2][32];
 #pragma unroll
         for (int q = 0; q < 2; ++q) tmem_ld32_async(sb + u * kSub + q * 32, v[q]);
@@ -1022,17 +1041,15 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
               for (int e = 0; e < 32; ++e)
                 if (!((keep >> e) & 1u)) v[q][e] = __float_as_uint(-INFINITY);
             }
-            if constexpr (SA) {  // of the new tokens, the later ones are left out
-              if ((q == 0 ? fresh.x : fresh.y) != 0u) {
-                const int4* tk = reinterpret_cast<const int4*>(key.toks + u * kSub + q * 32);
+            if constexpr (SA) {  // of the new tokens, the later ones are left out (branches here cost more)
+              const int4* tk = reinterpret_cast<const int4*>(key.toks + u * kSub + q * 32);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int4 y = tk[e];
-                  if (y.x > pos) v[q][4 * e] = __float_as_uint(-INFINITY);
-                  if (y.y > pos) v[q][4 * e + 1] = __float_as_uint(-INFINITY);
-                  if (y.z > pos) v[q][4 * e + 2] = __float_as_uint(-INFINITY);
-                  if (y.w > pos) v[q][4 * e + 3] = __float_as_uint(-INFINITY);
-                }
+              for (int e = 0; e < 8; ++e) {
+                const int4 y = tk[e];
+                if (y.x > pos) v[q][4 * e] = __float_as_uint(-INFINITY);
+                if (y.y > pos) v[q][4 * e + 1] = __float_as_uint(-INFINITY);
+                if (y.z > pos) v[q][4 * e + 2] = __float_as_uint(-INFINITY);
+                if (y.w > pos) v[q][4 * e + 3] = __float_as_uint(-INFINITY);
               }
             }
           }
@@ -1177,7 +1194,7 @@ __device__ void softmax_role(const Params& P, bool more, const Shared* seg, cons
 }
 
 template <int D, int NS, bool SA>
-__global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_kernel(const __grid_constant__ Params P) {
   using BR = Bars<NS>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Start s_start;
@@ -1219,13 +1236,10 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // SA: this much may run beside the order kernel (and whatever went before it);
-  // SWA: the order kernel may run beside the rest.
-  if (SA) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  } else {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  }
+  // SA: this much may run beside the order kernel (and whatever went before it)
+  if (SA) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the order kernel, or the kernel for the requests of few new tokens
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 64 && P.desc != nullptr) P.desc[blockIdx.x].valid = 0;
   if (warp == 0) {
     const Start s = find_start<SA>(P);
@@ -1245,7 +1259,7 @@ __global__ void __launch_bounds__(kThreads, 1) sa_paged_tiles_kernel(const __gri
   const Shared* seg = reinterpret_cast<const Shared*>(smem + P.off_seg);
   const auto* keys = reinterpret_cast<const typename KeysOf<SA>::T*>(smem + P.off_bad);
 
-  if (warp >= kFirstSoftmaxWarp) {
+  if (warp >= kFirstSoftmaxWarp && warp < kFirstSoftmaxWarp + 8) {
     softmax_role<D, NS, SA>(P, any, seg, keys, tmem, bars, abort_flag);
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     mma_role<D, NS, SA>(P, warp - kMmaWarp, any, seg, keys, sbase, tmem, bars, abort_flag);
@@ -1352,17 +1366,8 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
                     kMaxSmem, "shared memory");
   cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS, SA>>(smem);
   if (ce != cudaSuccess) return ce;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = SA ? 1 : 0;
-  ce = cudaLaunchKernelEx(&cfg, sa_paged_tiles_kernel<D, NS, SA>, P);
+  ce = launch_kernel(sa_paged_tiles_kernel<D, NS, SA>, dim3(unsigned(sms)), SA ? kSaThreads : kThreads, smem, stream,
+                     SA, P);
   if (ce != cudaSuccess || P.desc == nullptr) return ce;
   sa_paged_tiles_join_kernel<D, SA><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
   return cudaGetLastError();

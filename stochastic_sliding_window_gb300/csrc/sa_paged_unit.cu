@@ -25,7 +25,7 @@ constexpr int kMostKeys = 1280;
 constexpr int kRounds = kMostKeys / kUnitThreads + 1;  // window entries per thread
 
 template <int D, int PATH, int NT>
-__global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void unit(const Params& P) {
   constexpr int kPitch = Pitch<D>;
   constexpr int kCpr = D / 8;
   constexpr uint32_t kStageBytes = 2 * kKeys * kPitch;
@@ -259,11 +259,16 @@ __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __
 }
 
 template <int D, int PATH, int NT>
+__global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __grid_constant__ Params P) {
+  unit<D, PATH, NT>(P);
+  end_beside();
+}
+
+template <int D, int PATH, int NT>
 static cudaError_t launch_rows_of(const Params& P, unsigned grid, uint32_t smem, cudaStream_t stream) {
   const cudaError_t ce = allow_smem<sa_paged_unit_kernel<D, PATH, NT>>(200u * 1024);
   if (ce != cudaSuccess) return ce;
-  sa_paged_unit_kernel<D, PATH, NT><<<grid, kUnitThreads, smem, stream>>>(P);
-  return cudaGetLastError();
+  return launch_kernel(sa_paged_unit_kernel<D, PATH, NT>, dim3(grid), kUnitThreads, smem, stream, P.beside, P);
 }
 
 template <int D, int PATH>
