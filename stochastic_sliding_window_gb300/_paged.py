@@ -15,6 +15,16 @@ from typing import NamedTuple
 from . import _libsa
 from ._libsa import _check, _check_err, _need, _shape
 
+_torch = None  # set by the first call (the package imports without it)
+
+
+def _get_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 PAGED_AUTO, PAGED_ROWS, PAGED_TILES = 0, 1, 2
 _SWA, _SA, _GATED = 0, 1, 2
 
@@ -82,10 +92,10 @@ class _On:
     __slots__ = ("guards", "index")
 
     def __init__(self, index, stream):
-        import torch
+        torch = _torch
         self.index = index
         self.guards = ()
-        if index != torch.cuda.current_device():
+        if index != torch._C._cuda_getDevice():
             self.guards = (torch.cuda.device(index),)
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
@@ -95,10 +105,9 @@ class _On:
             self.guards += (torch.cuda.stream(stream),)
 
     def __enter__(self):
-        import torch
         for g in self.guards:
             g.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
+        return _torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -118,14 +127,15 @@ def _rows(t, name, dtype, ndim):
 def _tokens(t, name):
     """bf16 [T, H, d] whose rows [H, d] are contiguous; returns its shape and
     the stride between tokens."""
-    import torch
+    torch = _torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    n, h, d = shape = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(shape)}")
+    n, h, d = shape
     if t.is_contiguous():
         return shape, h * d
     st = t.stride()
@@ -137,12 +147,13 @@ def _tokens(t, name):
 def _caches(k_cache, v_cache):
     """Both caches, bf16 [pages, page_size, Hkv, d], pages contiguous and the
     same stride apart; returns their shape and that stride."""
-    import torch
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    torch = _torch
+    if not isinstance(k_cache, torch.Tensor) or not isinstance(v_cache, torch.Tensor):
+        raise TypeError(f"{'v' if isinstance(k_cache, torch.Tensor) else 'k'}_cache must be a torch.Tensor")
+    bf16 = torch.bfloat16
+    if k_cache.dtype is not bf16 or v_cache.dtype is not bf16:
+        name, t = ("v_cache", v_cache) if k_cache.dtype is bf16 else ("k_cache", k_cache)
+        raise TypeError(f"{name} must be {bf16}, got {t.dtype}")
     shape = k_cache.shape
     if len(shape) != 4 or 0 in shape:
         raise ValueError(f"k_cache must be [num_pages, page_size, Hkv, d], got {tuple(shape)}")
@@ -164,21 +175,27 @@ def _caches(k_cache, v_cache):
     return shape, k_cache.stride(0)
 
 
-def _one_device(first, name0, *named):
-    """The CUDA device number that all tensors share."""
-    index = first.get_device() if first.is_cuda else -1
-    if index < 0:
-        raise ValueError(f"{name0} must be a CUDA tensor")
-    for name, t in named:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+def _one_device(names, *tensors):
+    """The CUDA device number that all tensors (None: not given) share; names:
+    theirs, for the message."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index or index < 0:
+            first = names.split()[0]
+            if index < 0:
+                raise ValueError(f"{first} must be a CUDA tensor")
+            name = next(n for n, x in zip(names.split(), tensors) if x is t)
+            raise ValueError(f"{name} must be on {tensors[0].device}, got {t.device}")
     return index
+
+
+_FORWARD = "q k_cache v_cache block_table q_start seq_lens perm inv_perm gate_sa gate_swa out err"
 
 
 def _forward(path, q, k_cache, v_cache, block_table, q_start, seq_lens, window, window_swa, max_new,
              softmax_scale, out, kernel, err, stream, perm=None, inv_perm=None, gate_sa=None,
              gate_swa=None):
-    import torch
+    torch = _torch or _get_torch()
     i32 = torch.int32
     qshape, q_stride = _tokens(q, "q")
     (pages, page_size, hkv, dk), page_stride = _caches(k_cache, v_cache)
@@ -206,10 +223,8 @@ def _forward(path, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 
         _shape(out, "out", qshape)
     if err is not None:
         _check_err(err)
-    index = _one_device(q, "q", ("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table),
-                        ("q_start", q_start), ("seq_lens", seq_lens), ("perm", perm),
-                        ("inv_perm", inv_perm), ("gate_sa", gate_sa), ("gate_swa", gate_swa),
-                        ("out", out), ("err", err))
+    index = _one_device(_FORWARD, q, k_cache, v_cache, block_table, q_start, seq_lens, perm, inv_perm,
+                        gate_sa, gate_swa, out, err)
     ref = byref(SaPagedParams(b, t, int(max_new), hq, hkv, d, page_size, pages, max_pages, int(window),
                               int(window_swa), perm_rows, perm_len, int(kernel), float(softmax_scale), 0,
                               q_stride, page_stride, block_table.data_ptr(), q_start.data_ptr(),
@@ -291,7 +306,7 @@ def paged_plan(new_lens, cached_lens, block_table, free_pages, num_free, page_si
     q_start [B+1], seq_lens [B], slots and positions [max_tokens] (-1 past the
     last token) and counts [3] = new tokens, pages taken, pages left.  If the
     step does not fit, nothing is planned and the error word says so."""
-    import torch
+    torch = _torch or _get_torch()
     i32 = torch.int32
     b, = _rows(new_lens, "new_lens", i32, 1)
     if _rows(cached_lens, "cached_lens", i32, 1)[0] != b:
@@ -307,14 +322,13 @@ def paged_plan(new_lens, cached_lens, block_table, free_pages, num_free, page_si
         raise ValueError("max_tokens must be >= 0")
     if err is not None:
         _check_err(err)
-    outs = [q_start, seq_lens, slots, positions, counts]
-    names, sizes = ("q_start", "seq_lens", "slots", "positions", "counts"), [b + 1, b, n, n, 3]
-    for name, t, size in zip(names, outs, sizes):
-        if t is not None and _rows(t, name, i32, 1)[0] != size:
-            _shape(t, name, (size,))
-    index = _one_device(new_lens, "new_lens", ("cached_lens", cached_lens), ("block_table", block_table),
-                        ("free_pages", free_pages), ("num_free", num_free), ("err", err),
-                        *zip(names, outs))
+    outs = (q_start, seq_lens, slots, positions, counts)
+    sizes = (b + 1, b, n, n, 3)
+    for i, t in enumerate(outs):
+        if t is not None and _rows(t, PagedPlan._fields[i], i32, 1)[0] != sizes[i]:
+            _shape(t, PagedPlan._fields[i], (sizes[i],))
+    index = _one_device("new_lens cached_lens block_table free_pages num_free err q_start seq_lens slots "
+                        "positions counts", new_lens, cached_lens, block_table, free_pages, num_free, err, *outs)
     lib = _libsa._lib or _libsa.load()
     with _On(index, stream) as s:
         if any(t is None for t in outs):  # what is not given, cut from one allocation
@@ -336,7 +350,7 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, rope_base: float
     the caches.  With rope_base > 1 the keys are rotated by positions (int32
     [T]) as rope_ does, and q (bf16 [T, Hq, d]) is rotated into q_out, which
     is returned; otherwise None is."""
-    import torch
+    torch = _torch or _get_torch()
     (t, hkv, d), ks = _tokens(k, "k")
     vshape, vs = _tokens(v, "v")
     if vshape != k.shape:
@@ -367,8 +381,8 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, rope_base: float
         raise ValueError("q_out is given without q")
     if err is not None:
         _check_err(err)
-    index = _one_device(k, "k", ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slots", slots),
-                        ("positions", positions), ("q", q), ("q_out", q_out), ("err", err))
+    index = _one_device("k v k_cache v_cache slots positions q q_out err", k, v, k_cache, v_cache, slots,
+                        positions, q, q_out, err)
     ref = byref(SaPagedAppendParams(t, hkv, hq, d, page_size, pages, ks, vs, qs, page_stride, rope_base,
                                     err.data_ptr() if err is not None else None))
     lib = _libsa._lib or _libsa.load()
