@@ -232,9 +232,13 @@ struct SaOrder {
   int cap;         // entries of one list
 };
 // Whether a request's SA path goes to the tile kernel: enough window keys in
-// all to be worth passing over its whole list.
+// all, five times its length, to be worth passing over its whole list.  Measured
+// (four requests, row kernel against order and tiles, us): at 4 times 105 to
+// 126, 60 to 66, 210 to 141 and 62 to 110, at 6 times 161 to 108, 48 to 52, 287 to
+// 183 and 84 to 89 for 32 q heads on 8 kv heads and 16 on 16 at lengths of 16384
+// and 4096, window 128.
 __host__ __device__ inline bool paged_sa_tiled(int n, int len, int half, int row_limit) {
-  return n > row_limit && (long long)n * (2LL * half + 1) >= len;
+  return n > row_limit && (long long)n * (2LL * half + 1) >= 5LL * len;
 }
 inline bool paged_order_supported(const PagedProblem& pb) { return pb.B <= 1 << 27; }  // eight blocks each
 size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit);

@@ -434,9 +434,16 @@ static PagedProblem make_problem(const sa_paged_params_t* p, Path path) {
 }
 
 // Which kernels a call runs.  A request with n new tokens has n g query rows
-// per kv head; up to kRowLimit of them go to the row kernel, whose warps take
-// 16 rows over a run of keys, more to the tile kernel, whose blocks take 256.
-constexpr int kRowLimit = 64;
+// per kv head.  The row kernel's warps take 16 rows over a run of keys, so that
+// more rows read the keys again; the tile kernel's blocks take 256.  Measured for
+// SWA (row against tile kernel, us; 32 q heads on 8 kv heads, d = 128): 16
+// requests over 16384 keys each, 16 rows 138 to 130, 32 rows 196 to 125, 64 rows
+// 275 to 118; 64 over 4096, 125 to 164, 179 to 143, 375 to 180; 16 with a window
+// of 512, 12 to 16, 16 to 16, 29 to 16.
+// A gated call with tiles runs two or three kernels after another: 48 rows of 16
+// requests, SA window 128, SWA window 256, 51 against 53 (2 requests 12 against
+// 28); SWA window 1024, 87 against 70.
+constexpr int kSwaRows = 16, kGatedRows = 64, kWideGatedRows = 32, kWideWindow = 512;
 
 struct Choice {
   bool tiles;     // SWA (or the gated pair's SWA term) of requests beyond row_limit by tiles
@@ -449,7 +456,10 @@ static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
   Choice c{false, false, true, false, 0x7fffffff};
   if (kernel != SA_PAGED_ROWS && paged_tiles_supported(pb)) {
     if (kernel == SA_PAGED_TILES) return Choice{true, false, false, false, 0};
-    const int limit = pb.g >= kRowLimit ? 1 : kRowLimit / pb.g;
+    const int most = path == kPathSWA                                        ? kSwaRows
+                     : path == kPathGated && pb.window_swa > kWideWindow ? kWideGatedRows
+                                                                             : kGatedRows;
+    const int limit = pb.g >= most ? 1 : most / pb.g;
     if (pb.max_new > limit) c = Choice{path != kPathSA, path != kPathSWA, true, false, limit};
     if (!paged_order_supported(pb)) c.sa_tiles = false;
   }

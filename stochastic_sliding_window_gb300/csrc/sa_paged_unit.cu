@@ -278,8 +278,13 @@ static cudaError_t launch_unit(const Params& P, unsigned grid, uint32_t smem, cu
 
 }  // namespace prow
 
-// Units of up to 1280 keys, fewer than the row kernel would need to keep every
-// warp of the GPU in work for a while (8 warps of each SM, four units each).
+// Units of up to 1280 keys (their list and stages fit two blocks to an SM).  Very
+// many of very few keys are left to the row kernel, whose warps go from unit to
+// unit without a block's latency for each; so are those of calls with tiles,
+// where most units would be empty blocks (a gated chunk took 142 us instead of
+// 114).  Measured (unit against row kernel, us; a token each, 32 q heads on 8 kv heads, d = 128): window 128, 8 requests
+// 4.8 to 11.5, 128 18 to 20, 1000 126 to 113; window 512, 128 53 to 59, 1000 325
+// to 367; window 1024, 8 14 to 17, 1000 598 to 687.
 bool paged_unit_fits(const PagedProblem& pb, Path path, int row_limit, int sms) {
   int tb, rg, rows;
   paged_unit_shape(pb, path, row_limit, &tb, &rg, &rows);
@@ -287,7 +292,8 @@ bool paged_unit_fits(const PagedProblem& pb, Path path, int row_limit, int sms) 
   const long long heads = (long long)pb.Hkv * rg;
   const long long units = (pb.T + tb - 1) / tb * heads;
   const long long most = path == kPathSWA ? min(pb.max_new, row_limit) : pb.max_new;
-  return units < 32LL * sms && (most + tb - 1) / tb * pb.B * heads <= 65536;
+  const bool few = units < 32LL * sms || (paged_unit_keys(pb, path, tb) > 256 && pb.max_new <= row_limit);
+  return few && (most + tb - 1) / tb * pb.B * heads <= 65536;
 }
 
 sa_status_t launch_paged_unit(const PagedProblem& pb, Path path, int row_limit, const float* swa_part,
