@@ -235,6 +235,11 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
   return s;
 }
 
+// a / b, both >= 0: in 32 bits where that is enough.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // SA: n counts the request's members (its new tokens in sigma's order) and its
 // keys are entries of the list of its tokens in that order.
 struct Request {
@@ -368,6 +373,8 @@ __device__ __forceinline__ void next_tile(const Params& P, Cursor& c) {
   } while (c.r.n == 0);
   c.nt = num_tiles(P, c.r);
 }
+// Whether a tile part follows the one that next_seg returned last.
+__device__ __forceinline__ bool more_segs(const Cursor& c) { return !c.done && c.pos < c.end; }
 // The next tile part of the run; false at its end.
 template <bool SA>
 __device__ __forceinline__ bool next_seg(const Params& P, Cursor& c, Seg& s) {
@@ -418,7 +425,7 @@ __device__ Start find_start(const Params& P) {
     tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   }
   Start s;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = quotient(total + gridDim.x - 1, gridDim.x);
   s.cut = P.desc != nullptr && total >= tiles * kCutChunks;
   s.begin = per * blockIdx.x;
   s.end = min(total, s.begin + per);
@@ -449,7 +456,7 @@ __device__ Start find_start(const Params& P) {
       const Request r = load_request<SA>(P, s.b, false);
       const int nt = num_tiles(P, r);
       const long long per_head = chunks_before<SA>(P, r, nt);
-      s.kvh = int(rel / per_head);
+      s.kvh = int(quotient(rel, per_head));
       rel -= s.kvh * per_head;
       // the last tile that starts at or before rel: 32 candidates at a time
       int lo = 0, hi = nt;  // lo starts at or before it, hi does not
@@ -517,8 +524,8 @@ __device__ __forceinline__ void load_run(const CUtensorMap* maps, uint32_t dst, 
 
 // Warp 0 brings Q, K and what the other roles need to know, warp 3 brings V.
 template <int D, int NS>
-__device__ void producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
-                              uint32_t bars, volatile int* abort_flag) {
+__device__ void producer_role(const Params& P, const Start& start, const Cursor& first, const Seg& first_seg, bool have,
+                              uint8_t* smem, uint32_t sbase, uint32_t bars, volatile int* abort_flag) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
   const int lane = threadIdx.x & 31;
@@ -530,15 +537,13 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
     const bool ok = bounded_wait(bars + 8 * bar, parity & 1u, P.timeout_cycles, P.err, abort_flag);
     return __all_sync(0xffffffffu, ok);
   };
-  Cursor cur = make_cursor<false>(P, start);
-  Seg s, ahead;
+  Cursor cur = first;
+  Seg s = first_seg;
   int n = 0, x = 0;    // chunks and tiles so far
   int nq = 0, nk = 0;  // Q loads and loads of this warp's stages begun
   bool ok = true;
-  bool more = next_seg<false>(P, cur, ahead);
-  for (; ok && more; ++x) {
-    s = ahead;
-    more = next_seg<false>(P, cur, ahead);
+  for (; ok && have; ++x) {
+    const bool more = more_segs(cur);
     const int lo = tile_lo<false>(P, s.r, s.grp), hi = tile_hi<false>(P, s.r, s.grp);
     const int i0 = s.grp * P.Bt;
     const int32_t* table = P.table + (long long)s.b * P.max_pages;
@@ -658,6 +663,7 @@ __device__ void producer_role(const Params& P, const Start& start, uint8_t* smem
       ++nk;
       if (c + 1 < s.c1) page = page_at(int(unsigned(j0 + kKC) / unsigned(P.page)) + lane);
     }
+    have = more && next_seg<false>(P, cur, s);
   }
   // A block must not exit with copies in flight (after a failed wait nobody
   // else may be left to wait for them): each barrier's last use, bounded.
@@ -682,8 +688,9 @@ constexpr int kSaProducers = 128;
 static_assert(kSaProducers == kKC, "a key a thread");
 
 template <int D, int NS>
-__device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* smem, uint32_t sbase,
-                                 uint32_t bars, volatile int* abort_flag, volatile int* vote) {
+__device__ void sa_producer_role(const Params& P, const Start& start, const Cursor& first, const Seg& first_seg,
+                                 bool have, uint8_t* smem, uint32_t sbase, uint32_t bars,
+                                 volatile int* abort_flag, volatile int* vote) {
   using BR = Bars<NS>;
   constexpr uint32_t kTile = kKC * D * 2;
   constexpr int CPR = D / 8;               // 16-byte chunks per row
@@ -729,14 +736,12 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
       }
     }
   };
-  Cursor cur = make_cursor<true>(P, start);
-  Seg s, ahead;
+  Cursor cur = first;
+  Seg s = first_seg;
   int n = 0, x = 0;
   bool ok = true;
-  bool more = next_seg<true>(P, cur, ahead);
-  for (; ok && more; ++x) {
-    s = ahead;
-    more = next_seg<true>(P, cur, ahead);
+  for (; ok && have; ++x) {
+    const bool more = more_segs(cur);
     const int lo = tile_lo<true>(P, s.r, s.grp), hi = tile_hi<true>(P, s.r, s.grp);
     const int m0 = s.r.q0 + s.grp * P.Bt, nt = min(P.Bt, s.r.n - s.grp * P.Bt);
     const uint2* list = P.order.list + (long long)P.order.info[s.b].x * P.order.cap;
@@ -830,6 +835,7 @@ __device__ void sa_producer_role(const Params& P, const Start& start, uint8_t* s
       rows_in(vbase, sbase + P.off_v + uint32_t(st) * kTile + col, rows);
       cp_async_arrive_noinc(bars + 8 * (BR::kVfull + st));
     }
+    have = more && next_seg<true>(P, cur, s);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // own copies land before exit
 }
@@ -1198,6 +1204,8 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
   using BR = Bars<NS>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Start s_start;
+  __shared__ Cursor s_cursor;
+  __shared__ Seg s_seg;
   __shared__ bool s_any;
   __shared__ int s_vote[2];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1229,6 +1237,11 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (!SA && warp == 3) {
+    const int lane = threadIdx.x & 31, i = lane % kBoxes;  // (no boxes longer than a page)
+    const CUtensorMap* m = lane == 2 * kBoxes ? &P.tq : lane < kBoxes ? &P.tk[i] : &P.tv[i];
+    if (lane == 2 * kBoxes || (lane < 2 * kBoxes && 1 << i <= P.page))
+      asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   } else if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(tmem_slot)),
@@ -1248,6 +1261,8 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
     const bool any = next_seg<SA>(P, cur, seg);
     if (threadIdx.x == 0) {
       s_start = s;
+      s_cursor = cur;
+      s_seg = seg;
       s_any = any;
     }
   }
@@ -1264,9 +1279,9 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     mma_role<D, NS, SA>(P, warp - kMmaWarp, any, seg, keys, sbase, tmem, bars, abort_flag);
   } else if (SA) {
-    sa_producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag, s_vote);
+    sa_producer_role<D, NS>(P, s_start, s_cursor, s_seg, any, smem, sbase, bars, abort_flag, s_vote);
   } else {
-    producer_role<D, NS>(P, s_start, smem, sbase, bars, abort_flag);
+    producer_role<D, NS>(P, s_start, s_cursor, s_seg, any, smem, sbase, bars, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
