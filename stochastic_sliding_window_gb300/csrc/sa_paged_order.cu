@@ -17,7 +17,7 @@
 // registers between the count and the writing; longer rows of sigma are read a
 // second time.  Two requests of 1024 new tokens, 32768 places: 38 us of 180 for
 // the gated call with one block per request, whose members were placed by
-// binary searches; now the call takes 140, with the order found beside the SWA
+// binary searches; then the call took 140, with the order found beside the SWA
 // tiles.
 #include "sa_internal.h"
 

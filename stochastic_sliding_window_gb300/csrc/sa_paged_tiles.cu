@@ -23,11 +23,11 @@
 // heads on 8 kv heads, d = 128: 1.06 PFLOP; 568 us at cuBLAS's burst rate):
 //   one MMA warp, softmax over 128 columns at once         857-880 us (one producer)
 //   64-key parts, two MMA warps, softmax loop unrolled         935 us
-//   the same, the loop over the parts not unrolled         854-875 us, two producers 797-834
+//   the same, the loop over the parts not unrolled         854-875 us, two producers and a shorter start 745-805
 //   S of all 128 keys by one MMA of N = 128, P in parts        937 us
 //   the halves taking turns, 16 softmax warps in pairs         882 us
 // The unrolled softmax loop does not fit the instruction cache beside the
-// other roles' code.  What is left between 817 and the tensor cores' time is
+// other roles' code.  What is left between 770 and the tensor cores' time is
 // the chain S -> softmax -> P V -> S of a part (1900 cycles, of which 640 are
 // the MMAs of one half).
 //
@@ -57,7 +57,7 @@
 //               boxes of 64, 16, 4 and 1 rows, nine rounds of them for a ragged
 //               run, took 5400 cycles a chunk where pages of 48 tokens end
 //               anywhere: 78.5 us for the mixed batch against 58, and 857
-//               against 817 for the long prompt.)
+//               against 815 for the long prompt.)
 //               SA: warps 0, 3, 12 and 13, rows from anywhere by cp.async
 //   warps 1, 2  the elected lane issues the MMAs of half 0, of half 1; warp 1
 //               owns TMEM
