@@ -702,14 +702,8 @@ extern "C" sa_status_t sa_paged_append(const sa_paged_append_params_t* p, const 
   const int half = d / 2;
   if (rope) {
     const double inv_two_pi = 0.15915494309189533576888376337251;
-    // base^(-2 i / d) as a product of two powers: two roundings more, relative
-    // 2^-52 in all, and a quarter of the pow calls (25 ns each)
-    double low[8];
-    for (int j = 0; j < 8; ++j) low[j] = std::pow(p->rope_base, -2.0 * j / d);
-    for (int i = 0; i < half; i += 8) {
-      const double high = std::pow(p->rope_base, -2.0 * i / d) * inv_two_pi;
-      for (int j = 0; j < 8 && i + j < half; ++j) P.freq[i + j] = uint64_t(std::ldexp(high * low[j], 64));
-    }
+    for (int i = 0; i < half; ++i)
+      P.freq[i] = uint64_t(std::ldexp(std::pow(p->rope_base, -2.0 * i / d) * inv_two_pi, 64));
   }
   const bool vec = d % 16 == 0 && aligned(k, 16) && aligned(v, 16) && aligned(k_cache, 16) &&
                    aligned(v_cache, 16) && (!with_q || (aligned(q, 16) && aligned(q_out, 16))) &&

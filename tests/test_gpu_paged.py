@@ -492,6 +492,33 @@ def test_append(d, hkv, hq, page, shift, rope):
     assert (f(out)[rest] == 4.0).all()
 
 
+@pytest.mark.parametrize("d,hkv,hq,t", [(80, 2, 5, 700), (16, 8, 32, 2000), (256, 40, 4, 31), (48, 1, 1, 3000),
+                                        (64, 70, 140, 10), (128, 1, 1, 1300), (96, 3, 7, 1), (64, 8, 32, 1000)])
+def test_append_of_many_shapes(d, hkv, hq, t):
+    """Heads that the threads of a block take in one round or in several, with
+    threads over, and one or several tokens to a block.  (Tolerance as in
+    test_append, at positions below 2^15, where the frequencies' rounding is
+    less than the angle's.)"""
+    rng = np.random.default_rng(d + t)
+    qkv = bf16(rng.standard_normal((t, hq + 2 * hkv, d)))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    kc = torch.zeros(t // 16 + 1, 16, hkv, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    slots, positions = rng.permutation(kc.shape[0] * 16)[:t], rng.integers(0, 1 << 15, t)
+    err = err_word()
+    out = sa.paged_append(k, v, kc, vc, i32(slots), i32(positions), rope_base=500.0, q=q, err=err)
+    assert sa.check_error(err) == sa.SA_OK
+    f = lambda x: x.float().cpu().numpy().astype(np.float64)
+    for have, x in ((f(kc).reshape(-1, hkv, d)[slots], f(k)), (f(out), f(q))):
+        want = oracle.rotate_at(x, positions, 500.0)
+        size = np.hypot(x[..., :d // 2], x[..., d // 2:])
+        rel = 2 * 2.0 ** -22 + 2 * np.pi * 2.0 ** -32 + np.pi * 2.0 ** -24 + 2 * 2.0 ** -23 + 4 * 2.0 ** -24
+        bar = rel * np.concatenate([size, size], -1)
+        bar = bar + 2.0 ** -8 * (np.abs(want) + bar)
+        assert (np.abs(have - want) <= bar).all()
+    assert np.array_equal(f(vc).reshape(-1, hkv, d)[slots], f(v))
+
+
 def test_append_agrees_with_rope_on_a_sequence():
     """Positions 0 .. n-1: the same rotation as rope_, up to one rounding step
     of bf16 where the two angles' last bits differ."""
@@ -610,6 +637,47 @@ def test_captured_graph_reads_the_lengths_of_its_replay(path):
         graph.replay()
         src.check(out, path, 20, 30, what=path)
     assert sa.check_error(err) == sa.SA_OK
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("path", ["swa", "sa", "gated"])
+def test_what_follows_a_call_finds_all_of_it_done(path, captured):
+    """A call's kernels may run beside each other; whatever comes next in the
+    stream may not: it reads whole results, and may overwrite the inputs."""
+    new, total = [300, 1, 1, 700, 2, 1], [2100, 900, 1500, 1400, 33, 1]
+    b = Batch(new, total, 8, 2, 128, 48, seed=12, perm_len=2200)
+    out = torch.empty(b.t, 8, 128, dtype=torch.bfloat16, device="cuda")
+    err = err_word()
+    kept = [torch.empty_like(out) for _ in range(3)]
+    inputs = [b.k, b.v, b.args[4]]
+    saved = [x.clone() for x in inputs]
+    spoiled = [torch.full_like(x, 7) for x in inputs]
+
+    def step():
+        for x in kept:
+            for t, y in zip(inputs, saved):
+                t.copy_(y)
+            b.run(path, 300, 1000, out=out, err=err, max_new=700)
+            for t, y in zip(inputs, spoiled):
+                t.copy_(y)
+            x.copy_(out)
+            out.zero_()
+
+    step()
+    if captured:
+        torch.cuda.synchronize()
+        for x in kept:
+            x.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        graph.replay()
+        graph.replay()
+    for t, y in zip(inputs, saved):
+        t.copy_(y)
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(kept[0], path, 300, 1000, weight_bits=8, what=path)
+    assert torch.equal(kept[0], kept[1]) and torch.equal(kept[0], kept[2])
 
 
 def test_given_streams():
