@@ -1,5 +1,6 @@
-"""ctypes binding of libsa's serving calls: attention over a paged K/V cache,
-the plan of a step and the writer of new tokens.
+"""Binding of libsa's serving calls: attention over a paged K/V cache, the plan
+of a step and the writer of new tokens.  The usual arguments take the short way
+(``csrc/paged_call.cpp``), whatever else the long one, through ctypes.
 
 Argument marshalling only, as in ``_libsa``: types, shapes and devices are
 checked here, lengths, tables and sigma (device data) by the kernels, which
@@ -23,6 +24,25 @@ def _get_torch():
     import torch
     _torch = torch
     return torch
+
+
+_native = None  # paged_call.cpp's module; False: not built
+
+
+def _get_native():
+    global _native
+    lib = _libsa._lib or _libsa.load()
+    _get_torch()
+    try:
+        from . import _paged_call as native
+    except ImportError:
+        _native = False
+        return False
+    native.bind(*[ctypes.cast(f, c_void_p).value for f in (
+        lib.swa_paged_forward, lib.sa_paged_forward, lib.sa_swa_gated_paged_forward,
+        lib.sa_paged_workspace_size, lib.sa_paged_plan, lib.sa_paged_append)])
+    _native = native
+    return native
 
 
 PAGED_AUTO, PAGED_ROWS, PAGED_TILES = 0, 1, 2
@@ -189,6 +209,17 @@ def _one_device(names, *tensors):
     return index
 
 
+def _short(path, *args):
+    """The short way of a forward call; None: the long one is needed."""
+    native = _get_native() if _native is None else _native
+    if not native:
+        return None
+    r = native.forward(path, *args)
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
 _FORWARD = "q k_cache v_cache block_table q_start seq_lens perm inv_perm gate_sa gate_swa out err"
 
 
@@ -268,6 +299,11 @@ def swa_paged_forward(q, k_cache, v_cache, block_table, q_start, seq_lens, windo
     request, where the caller knows one (1 when decoding).  Rows of out that
     no request has are left as they were (uninitialised if out is not given).
     """
+    if stream is None:
+        r = _short(_SWA, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 0, max_new, softmax_scale,
+                   out, kernel, err, None, None, None, None)
+        if r is not None:
+            return r
     return _forward(_SWA, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 0, max_new,
                     softmax_scale, out, kernel, err, stream)
 
@@ -282,6 +318,11 @@ def sa_paged_forward(q, k_cache, v_cache, block_table, q_start, seq_lens, perm, 
     inverse (sa_inverse_perm).  The rows equal those of sa_forward(causal=True)
     on the whole sequence.  The rest as in swa_paged_forward.
     """
+    if stream is None:
+        r = _short(_SA, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 0, max_new, softmax_scale,
+                   out, kernel, err, perm, inv_perm, None, None)
+        if r is not None:
+            return r
     return _forward(_SA, q, k_cache, v_cache, block_table, q_start, seq_lens, window, 0, max_new,
                     softmax_scale, out, kernel, err, stream, perm, inv_perm)
 
@@ -292,6 +333,11 @@ def sa_swa_gated_paged_forward(q, k_cache, v_cache, block_table, q_start, seq_le
                                kernel: int = PAGED_AUTO, err=None, stream=None):
     """sigmoid(gate_sa) * SA + sigmoid(gate_swa) * SWA over a paged cache; the
     gate logits (fp32 [T, Hq]) are the new tokens'."""
+    if stream is None:
+        r = _short(_GATED, q, k_cache, v_cache, block_table, q_start, seq_lens, window, window_swa, max_new,
+                   softmax_scale, out, kernel, err, perm, inv_perm, gate_sa, gate_swa)
+        if r is not None:
+            return r
     return _forward(_GATED, q, k_cache, v_cache, block_table, q_start, seq_lens, window, window_swa,
                     max_new, softmax_scale, out, kernel, err, stream, perm, inv_perm, gate_sa, gate_swa)
 
@@ -306,6 +352,14 @@ def paged_plan(new_lens, cached_lens, block_table, free_pages, num_free, page_si
     q_start [B+1], seq_lens [B], slots and positions [max_tokens] (-1 past the
     last token) and counts [3] = new tokens, pages taken, pages left.  If the
     step does not fit, nothing is planned and the error word says so."""
+    if stream is q_start is seq_lens is slots is positions is counts is None:
+        native = _get_native() if _native is None else _native
+        r = native.plan(new_lens, cached_lens, block_table, free_pages, num_free, page_size, num_pages,
+                        max_tokens, err) if native else None
+        if r is not None:
+            if r.__class__ is int:
+                _check(r)
+            return PagedPlan._make(r)
     torch = _torch or _get_torch()
     i32 = torch.int32
     b, = _rows(new_lens, "new_lens", i32, 1)
@@ -350,6 +404,15 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, rope_base: float
     the caches.  With rope_base > 1 the keys are rotated by positions (int32
     [T]) as rope_ does, and q (bf16 [T, Hq, d]) is rotated into q_out, which
     is returned; otherwise None is."""
+    if stream is None:
+        native = _get_native() if _native is None else _native
+        r = native.append(k, v, k_cache, v_cache, slots, positions, rope_base, q, q_out, err) if native else None
+        if r is not None:
+            if r is True:
+                return None
+            if r.__class__ is int:
+                _check(r)
+            return r
     torch = _torch or _get_torch()
     (t, hkv, d), ks = _tokens(k, "k")
     vshape, vs = _tokens(v, "v")

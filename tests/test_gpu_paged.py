@@ -680,6 +680,78 @@ def test_what_follows_a_call_finds_all_of_it_done(path, captured):
     assert torch.equal(kept[0], kept[1]) and torch.equal(kept[0], kept[2])
 
 
+@pytest.fixture(params=["short", "long"])
+def way(request, monkeypatch):
+    """Both ways from Python into the library."""
+    from stochastic_sliding_window_gb300 import _paged
+    _paged._get_native()
+    assert _paged._native, "paged_call.cpp was not built"
+    if request.param == "long":
+        monkeypatch.setattr(_paged, "_native", False)
+    return request.param
+
+
+def test_both_ways_take_the_same_arguments(way, monkeypatch):
+    from stochastic_sliding_window_gb300 import _paged
+    shapes = dict(stride_q=64, pair_pages=True, behind=2)
+    b = Batch([1, 3, 40], [700, 90, 41], 8, 2, 128, 16, seed=6, perm_len=800, **shapes)
+    out = torch.zeros(b.t + 2, 8, 128, dtype=torch.bfloat16, device="cuda")
+    err = err_word()
+    for path in ("swa", "sa", "gated"):
+        kw = dict(max_new=40, softmax_scale=0.25, err=err)
+        got = b.run(path, 30, 50, **kw)
+        assert b.run(path, 30, 50, out=out, **kw) is out
+        assert got.shape == out.shape and got.dtype == torch.bfloat16 and not got.requires_grad
+        b.check(got, path, 30, 50, weight_bits=8, scale=0.25, what=path)
+        # (np.int64 is no int: the long way)
+        assert torch.equal(b.run(path, np.int64(30), 50, **kw)[:b.t], got[:b.t])
+        with monkeypatch.context() as m:
+            m.setattr(_paged, "_native", False)
+            assert torch.equal(b.run(path, 30, 50, **kw)[:b.t], got[:b.t])
+    assert sa.check_error(err) == sa.SA_OK
+
+
+def test_both_ways_plan_and_append(way):
+    table, free = i32(np.full((2, 4), -1)), i32(np.arange(9))
+    p = sa.paged_plan(i32([5, 1]), i32([0, 0]), table, free, i32([9]), page_size=4, num_pages=9, max_tokens=7)
+    assert p._fields == ("q_start", "seq_lens", "slots", "positions", "counts")
+    assert [x.tolist() for x in p] == [[0, 5, 6], [5, 1], [32, 33, 34, 35, 28, 24, -1], [0, 1, 2, 3, 4, 0, -1], [6, 3, 6]]
+    assert all(x.is_contiguous() and x.dtype == torch.int32 for x in p)
+    kv = bf16(np.random.default_rng(0).standard_normal((7, 2, 3, 64)))
+    kc = torch.zeros(9, 4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    assert sa.paged_append(kv[:, 0], kv[:, 1], kc, vc, p.slots) is None
+    rows = p.slots[:6].long()
+    assert torch.equal(kc.view(-1, 3, 64)[rows], kv[:6, 0]) and torch.equal(vc.view(-1, 3, 64)[rows], kv[:6, 1])
+    q = sa.paged_append(kv[:, 0], kv[:, 1], kc, vc, p.slots, p.positions, rope_base=100, q=kv[:, 1])
+    assert q.shape == (7, 3, 64) and torch.equal(q[:1], kv[:1, 1])
+    assert sa.paged_append(kv[:, 0], kv[:, 1], kc, vc, p.slots, p.positions, rope_base=100.0, q=kv[:, 1], q_out=q) is q
+
+
+def test_both_ways_refuse(way):
+    b = Batch([1, 3], [70, 9], 8, 2, 64, 16, seed=6, perm_len=80)
+    q, k, v, table, start, lens = b.args
+    run = lambda *a, **kw: sa.sa_paged_forward(*a, b.perm_d, b.inv_d, **{"window": 4, **kw})
+    for bad, kind in [((q.float(), k, v, table, start, lens), TypeError), ((q, k, v.half(), table, start, lens), TypeError),
+                      ((q, k, v[:, :8], table, start, lens), ValueError), ((q, k, v, table.long(), start, lens), TypeError),
+                      ((q, k, v, table[:1], start, lens), ValueError), ((q, k, v, table, start[:2], lens), ValueError),
+                      ((q, k, v, table.cpu(), start, lens), ValueError), ((q.cpu(), k, v, table, start, lens), ValueError),
+                      ((q[:, :, :32], k, v, table, start, lens), ValueError), ((None, k, v, table, start, lens), TypeError)]:
+        with pytest.raises(kind):
+            run(*bad)
+    for kw in (dict(window=0), dict(kernel=9), dict(kernel=sa.PAGED_TILES), dict(out=q)):
+        with pytest.raises(RuntimeError):
+            run(*b.args, **kw)
+    with pytest.raises(ValueError):
+        run(*b.args, out=torch.empty(3, 8, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(TypeError):
+        run(*b.args, err=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError):
+        sa.paged_plan(i32([1]), i32([0]), table, i32([0]), i32([1]), page_size=4, num_pages=1, max_tokens=1)
+    with pytest.raises(ValueError):
+        sa.paged_append(k[0, :1], v[0, :1], k, v, i32([0]), rope_base=10.0)
+
+
 def test_given_streams():
     """A call on a stream of its own, ordered by the caller."""
     b = Batch([1, 1], [700, 90], 8, 2, 128, 16, seed=6)
