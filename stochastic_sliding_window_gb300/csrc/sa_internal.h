@@ -144,12 +144,13 @@ cudaError_t allow_smem(uint32_t bytes) {
   return ce;
 }
 
-// Launches a kernel; `beside`: it may start while the kernel before it in the
-// stream still runs (once each block of that one allows it or has ended), and
-// orders itself with griddepcontrol.wait.
+// Launches a kernel that may be set up while the kernel before it in the stream
+// still runs (once each block of that one allows it or has ended), and orders
+// itself: by begin_after or begin_alone, or by end_beside.  early = false: not before that one
+// has ended.
 template <class P>
 cudaError_t launch_kernel(void (*kernel)(P), dim3 grid, unsigned threads, uint32_t smem, cudaStream_t stream,
-                          bool beside, const P& params) {
+                          const P& params, bool early = true) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -159,10 +160,20 @@ cudaError_t launch_kernel(void (*kernel)(P), dim3 grid, unsigned threads, uint32
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = beside ? 1 : 0;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, params);
 }
 #ifdef __CUDACC__
+// The start of a kernel (all its threads): what came before it is done, and the
+// next one may be set up.
+__device__ __forceinline__ void begin_after() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// The same, but the next one is not set up before this one's blocks have ended:
+// where nothing is gained by it (a plan of 1500 requests 10.5 us a call instead
+// of 13.8, an append of 128 tokens 5.9 instead of 6.4).
+__device__ __forceinline__ void begin_alone() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The end of a kernel that needs nothing of the one that it runs beside: its
 // last block outlasts that one, so who waits for this kernel waits for both.
 __device__ __forceinline__ void end_beside() {

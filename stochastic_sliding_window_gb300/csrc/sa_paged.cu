@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) sa_paged_plan_kernel(const __gri
   __shared__ int s_scan[2][kPlanThreads / 32];
   __shared__ int s_start[kPlanThreads + 1], s_take[kPlanThreads];
   __shared__ int s_cached[kPlanThreads], s_row[kPlanThreads];
+  begin_alone();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = P.page;
   const int nfree = *P.num_free;
@@ -265,6 +266,7 @@ __device__ __forceinline__ int append_slot(const AppendParams& P, int t) {
 template <bool kVec>
 __global__ void __launch_bounds__(kAppendThreads, 8) sa_paged_append_kernel(const __grid_constant__ AppendParams P) {
   __shared__ __align__(16) float2 s_cs[kMaxAngles];
+  begin_alone();
   const int half = P.d / 2;
   const int t0 = blockIdx.x * P.tpb;
   const int ntok = min(P.tpb, P.T - t0);
@@ -640,8 +642,8 @@ extern "C" sa_status_t sa_paged_plan(const int32_t* new_lens, const int32_t* cac
   P.num_pages = num_pages;
   P.max_tokens = max_tokens;
   const int grid = max_tokens > paged::kTokens ? (max_tokens + paged::kTokens - 1) / paged::kTokens : 1;
-  paged::sa_paged_plan_kernel<<<grid, paged::kPlanThreads, 0, stream>>>(P);
-  const cudaError_t ce = cudaGetLastError();
+  const cudaError_t ce =
+      launch_kernel(paged::sa_paged_plan_kernel, dim3(unsigned(grid)), paged::kPlanThreads, 0, stream, P);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(ce));
   return succeed();
 }
@@ -729,11 +731,8 @@ extern "C" sa_status_t sa_paged_append(const sa_paged_append_params_t* p, const 
   P.tpb = tpb < 1 ? 1 : tpb;
   P.gpt = groups / P.tpb;
   const unsigned grid = unsigned((p->tokens + P.tpb - 1) / P.tpb);
-  if (vec)
-    sa_paged_append_kernel<true><<<grid, kAppendThreads, 0, stream>>>(P);
-  else
-    sa_paged_append_kernel<false><<<grid, kAppendThreads, 0, stream>>>(P);
-  const cudaError_t ce = cudaGetLastError();
+  const cudaError_t ce = launch_kernel(vec ? sa_paged_append_kernel<true> : sa_paged_append_kernel<false>, dim3(grid),
+                                       kAppendThreads, 0, stream, P);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "append launch: %s", cudaGetErrorString(ce));
   return succeed();
 }

@@ -42,7 +42,7 @@ struct Params {
   uint2* words;  // [lists][cap / 32] of each 32 places: which are in the list, entries before them
   int2* mark;    // [T] members in sigma's order, a request's from q_start on: place, position
   long long perm_stride, page_rows;
-  int T, max_new, max_pages, page, num_pages, perm_len, half, row_limit, Bt, Hkv, lists;
+  int T, max_new, max_pages, page, num_pages, perm_len, half, row_limit, Bt, Hkv, lists, beside;
 };
 
 __device__ __forceinline__ int new_tokens(const Params& P, int b, int* len) {
@@ -243,7 +243,11 @@ __device__ __forceinline__ void order_request(const Params& P) {
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     sa_paged_order_kernel(const __grid_constant__ Params P) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (P.beside) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    begin_after();
+  }
   order_request(P);
   end_beside();  // (the SWA tiles)
 }
@@ -301,8 +305,9 @@ sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_t
   P.Bt = tile_tokens;
   P.Hkv = pb.Hkv;
   P.lists = int(lists(pb, row_limit));
+  P.beside = beside;
   const cudaError_t ce =
-      launch_kernel(sa_paged_order_kernel, dim3(unsigned(pb.B) * kCluster), kThreads, 0, stream, beside, P);
+      launch_kernel(sa_paged_order_kernel, dim3(unsigned(pb.B) * kCluster), kThreads, 0, stream, P);
   if (ce != cudaSuccess) return fail(SA_ERR_CUDA, "paged order launch: %s", cudaGetErrorString(ce));
   return SA_OK;
 }

@@ -448,8 +448,11 @@ __device__ __forceinline__ void rows_role(const Params& P) {
 template <int D, int PATH, int NT>
 __global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
     sa_paged_rows_kernel(const __grid_constant__ Params P) {
-  // the join kernel's blocks may be put on SMs that this grid has left
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (P.beside) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    begin_after();
+  }
   rows_role<D, PATH, NT>(P);
   end_beside();
 }
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(32 * most_warps(D, NT), 1)
 // order: block c takes the unit that starts in worker c's run.
 template <int D, int PATH>
 __global__ void __launch_bounds__(128) sa_paged_join_kernel(const __grid_constant__ Params P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's writes
+  begin_after();
   const Desc d = P.desc[blockIdx.x];
   if (!d.valid) return;
   const int c0 = blockIdx.x;
@@ -547,7 +550,7 @@ static cudaError_t launch_rows(const Params& P, const Config& c, int sms, cudaSt
   const cudaError_t ce = allow_smem<sa_paged_rows_kernel<D, PATH, NT>>(kMaxSmem);
   if (ce != cudaSuccess) return ce;
   return launch_kernel(sa_paged_rows_kernel<D, PATH, NT>, dim3(unsigned(sms)), unsigned(32 * c.warps), smem, stream,
-                       P.beside, P);
+                       P);
 }
 
 template <int D, int PATH>
@@ -555,7 +558,7 @@ static cudaError_t launch_one(const Params& P, const Config& c, int sms, cudaStr
   const cudaError_t ce = c.R <= 8 ? launch_rows<D, PATH, 1>(P, c, sms, stream) : launch_rows<D, PATH, 2>(P, c, sms, stream);
   if (ce != cudaSuccess || c.snap) return ce;
   // its blocks may be set up while the row kernel's last ones finish
-  return launch_kernel(sa_paged_join_kernel<D, PATH>, dim3(unsigned(c.workers)), 128, 0, stream, true, P);
+  return launch_kernel(sa_paged_join_kernel<D, PATH>, dim3(unsigned(c.workers)), 128, 0, stream, P);
 }
 
 void fill_params(Params* out, const PagedProblem& pb, Path path, int row_limit, const float* swa_part) {

@@ -1249,10 +1249,7 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // SA: this much may run beside the order kernel (and whatever went before it)
-  if (SA) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the order kernel, or the kernel for the requests of few new tokens
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_after();  // (the order kernel, or the one for requests of few new tokens, may run beside the rest)
   if (threadIdx.x == 64 && P.desc != nullptr) P.desc[blockIdx.x].valid = 0;
   if (warp == 0) {
     const Start s = find_start<SA>(P);
@@ -1296,6 +1293,7 @@ __global__ void __launch_bounds__(SA ? kSaThreads : kThreads, 1) sa_paged_tiles_
 // (c, y) takes columns of the tile that starts in run c.
 template <int D, bool SA>
 __global__ void __launch_bounds__(kRows) sa_paged_tiles_join_kernel(const __grid_constant__ Params P) {
+  begin_after();
   const int c0 = blockIdx.x;
   const Desc d = P.desc[c0];
   if (!d.valid) return;
@@ -1381,11 +1379,12 @@ static cudaError_t launch_one(Params& P, int sms, cudaStream_t stream) {
                     kMaxSmem, "shared memory");
   cudaError_t ce = allow_smem<sa_paged_tiles_kernel<D, NS, SA>>(smem);
   if (ce != cudaSuccess) return ce;
+  // (a gated call's first kernel set up early made 123 us of 107: the order kernel
+  // and the SA tiles behind it find their SMs in another order)
   ce = launch_kernel(sa_paged_tiles_kernel<D, NS, SA>, dim3(unsigned(sms)), SA ? kSaThreads : kThreads, smem, stream,
-                     SA, P);
+                     P, SA || P.gate == nullptr);
   if (ce != cudaSuccess || P.desc == nullptr) return ce;
-  sa_paged_tiles_join_kernel<D, SA><<<dim3(unsigned(sms), D / 16), kRows, 0, stream>>>(P);
-  return cudaGetLastError();
+  return launch_kernel(sa_paged_tiles_join_kernel<D, SA>, dim3(unsigned(sms), D / 16), kRows, 0, stream, P);
 }
 
 }  // namespace ptile

@@ -261,6 +261,11 @@ __device__ __forceinline__ void unit(const Params& P) {
 
 template <int D, int PATH, int NT>
 __global__ void __launch_bounds__(kUnitThreads, 2) sa_paged_unit_kernel(const __grid_constant__ Params P) {
+  if (P.beside) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else {
+    begin_after();
+  }
   unit<D, PATH, NT>(P);
   end_beside();
 }
@@ -269,7 +274,7 @@ template <int D, int PATH, int NT>
 static cudaError_t launch_rows_of(const Params& P, unsigned grid, uint32_t smem, cudaStream_t stream) {
   const cudaError_t ce = allow_smem<sa_paged_unit_kernel<D, PATH, NT>>(200u * 1024);
   if (ce != cudaSuccess) return ce;
-  return launch_kernel(sa_paged_unit_kernel<D, PATH, NT>, dim3(grid), kUnitThreads, smem, stream, P.beside, P);
+  return launch_kernel(sa_paged_unit_kernel<D, PATH, NT>, dim3(grid), kUnitThreads, smem, stream, P);
 }
 
 template <int D, int PATH>
