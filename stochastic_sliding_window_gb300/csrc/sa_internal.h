@@ -220,7 +220,7 @@ long long paged_unit_keys(const PagedProblem& pb, Path path, int tb);
 // each; no workspace.
 bool paged_unit_fits(const PagedProblem& pb, Path path, int row_limit, int sms);
 sa_status_t launch_paged_unit(const PagedProblem& pb, Path path, int row_limit,
-                              const float* swa_part, cudaStream_t stream);
+                              const float* swa_part, int sms, cudaStream_t stream);
 
 // Tile kernel (sa_paged_tiles.cu): the SWA path of requests with more than
 // row_limit new tokens, into pb.out; with `gate` (logits [T, Hq]) as fp32

@@ -549,7 +549,7 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
   }
   pb.beside = (ch.tiles || ch.sa_tiles) && path != kPathGated;  // (gated: it adds the SWA tiles' part)
   if (ch.unit) {
-    st = launch_paged_unit(pb, path, ch.row_limit, swa_part, stream);
+    st = launch_paged_unit(pb, path, ch.row_limit, swa_part, sms, stream);
     if (st != SA_OK) return st;
   }
   if (ch.rows) {
