@@ -3,8 +3,8 @@
 // single-token calls take a few microseconds on the GPU, and reading a dozen
 // tensors' shapes and addresses through Python and ctypes, with caches that
 // the last launch has emptied, takes longer than that: one token of SWA 16.7 us
-// a call against 6.2 here (4.4 on the GPU), a plan of 64 tokens 28 against 7.7,
-// an append of 128 tokens 19 against 8.0.  Whatever is not as expected returns
+// a call against 4.6 to 6.2 here (4.1 on the GPU), a plan of 64 tokens 28 against
+// 5.9, an append of 128 tokens 19 against 6.0.  Whatever is not as expected returns
 // None, and the caller goes the long way, which says what is wrong.  The
 // functions of libsa.so are handed over by address (bind).
 #include <Python.h>

@@ -27,7 +27,7 @@ namespace paged {
 //
 // Bound by latency: two passes over the lengths (check, then scan), a search
 // and two dependent loads, then one 8-byte store per token.  A step of 64
-// single tokens takes 4.0 us on the GPU, 1500 requests with 250 000 tokens 13.
+// single tokens takes 4.0 us on the GPU, 1500 requests with 250 000 tokens 10.
 
 constexpr int kPlanThreads = 512;
 constexpr int kTokens = 1024;  // tokens per block
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) sa_paged_plan_kernel(const __gri
 // registers.  (With an item of any token and head at a time, found by
 // divisions, its angles read from shared memory, a thread spent 290
 // instructions per item and nine prompts of up to 4096 tokens took 163 us
-// against 114; 105 at the copy rate.  Four heads at a time spill at the 64
+// against 111; 105 at the copy rate.  Four heads at a time spill at the 64
 // registers of 8 blocks of 128 threads to an SM: 130 us.  Streaming loads and
 // stores took 110, but the attention that follows reads what is written here.)
 // The angle of position p at frequency f_k = base^(-2k/d) / (2 pi) turns per

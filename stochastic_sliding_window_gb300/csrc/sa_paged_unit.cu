@@ -11,8 +11,8 @@
 // once, leave out those of later tokens (an SA window of a sequence at half
 // its length holds half its keys), and put their rows' offsets in shared
 // memory; its warps take every fourth tile of 16 keys, and their sums meet in
-// shared memory at the end.  One token of one request, SWA window 128: 4.4 us on
-// the GPU, 10.5 by the row and join kernels; SA, 64 requests at 32768 places: 12.9.
+// shared memory at the end.  One token of one request, SWA window 128: 4.1 us on
+// the GPU, 10.5 by the row and join kernels; SA, 64 requests at 32768 places: 12.5.
 #include "sa_paged_rows.cuh"
 
 #include <cstring>
