@@ -858,6 +858,8 @@ __device__ void mma_role(const Params& P, int h, bool more, const Shared* seg, c
     return __all_sync(0xffffffffu, ok);
   };
   int np[2] = {0, 0}, xh = 0;  // O MMAs of each part, tile parts so far
+  // (P of a tile's first part says that the last tile's O has been read out, too;
+  // without the wait for that the long prompt took 795 us instead of 775)
   auto pv_ready = [&](int u, bool first) {
     return wait(BR::kPfull + 2 * h + u, uint32_t(np[u]++)) &&
            !(first && xh > 0 && !wait(BR::kOfree + h, uint32_t(xh - 1)));

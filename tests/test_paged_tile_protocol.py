@@ -7,8 +7,10 @@ chunk before and then S = Q K; four softmax warps per half that take S, may
 correct O, write P over it and read O out at the tile's end.  The tensor pipe
 runs MMAs in the order of their issue, so S may be issued over a P that an
 earlier MMA still has to read: S and P change hands when an MMA completes, not
-when it is issued.  Half 1 may have no rows or, for SA, only some of a tile's
-chunks; a tile's last chunk may have one part.
+when it is issued.  A tile's first P, of all four warps, also says that they
+have read the last tile's O out: the kernel's own wait for that is left out
+here.  Half 1 may have no rows or, for SA, only some of a tile's chunks; a
+tile's last chunk may have one part.
 """
 
 from __future__ import annotations
