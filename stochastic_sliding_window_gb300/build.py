@@ -30,7 +30,7 @@ CALL = PKG / "_paged_call.so"
 SOURCES = ["sa_api.cu", "sa_perm.cu", "sa_simt.cu", "sa_tc.cu", "sa_tc_ring.cu", "sa_tc_chunk.cu",
            "sa_bwd.cu", "sa_graph.cu", "sa_prologue.cu", "sa_shard.cu", "sa_paged.cu",
            "sa_paged_rows.cu", "sa_paged_unit.cu", "sa_paged_tiles.cu",
-           "sa_paged_order.cu"]
+           "sa_paged_order.cu", "sa_paged_members.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v"]

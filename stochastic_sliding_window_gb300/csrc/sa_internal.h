@@ -203,7 +203,7 @@ struct PagedProblem {
   void* out;
   int32_t* err;
   bool beside;               // the row or unit kernel runs beside the tile kernel
-  int sa_limit;              // requests with more new tokens may go to the SA tiles (paged_sa_tiled)
+  int sa_limit;              // requests with more new tokens may go over sigma's order (paged_sa_tiled)
 };
 
 // Row kernel (sa_paged_rows.cu).  Requests with more than row_limit new
@@ -232,33 +232,55 @@ sa_status_t launch_paged_tiles(const PagedProblem& pb, int row_limit, const floa
 int paged_tile_tokens(const PagedProblem& pb);  // tokens of a tile
 
 // The requests' tokens in sigma's order (sa_paged_order.cu), for those whose
-// SA path the tile kernel takes (paged_sa_tiled).
+// SA path the tile or member kernel takes (paged_sa_tiled).
 struct SaOrder {
   uint2* list;     // [requests taken][cap] tokens in sigma's order: row of the
                    // caches at kv head 0 (0xffffffff: bad page), position
   int4* members;   // [T] new tokens in sigma's order, a request's from q_start on:
                    // first and last list entry of the window, row, position
   int32_t* chunks; // [T + B] key chunks before each of a request's tiles, from q_start + b on
-  int2* info;      // [B] list number, members (0: not taken)
+  int4* info;      // [B] list number, members if the tile kernel takes the request, if the member kernel does
+  int2* groups;    // [T / group + B] request and number of a group of its members (-1: none; not
+                   // written where q_start is bad), a request's from q_start / group + b on
+  int group;       // members of one (0: no groups)
   int cap;         // entries of one list
 };
-// Whether a request's SA path goes to the tile kernel: enough window keys in
-// all, five times its length, to be worth passing over its whole list.  Measured
-// (four requests, row kernel against order and tiles, us): at 4 times 105 to
-// 126, 60 to 66, 210 to 141 and 62 to 110, at 6 times 161 to 108, 48 to 52, 287 to
-// 183 and 84 to 89 for 32 q heads on 8 kv heads and 16 on 16 at lengths of 16384
-// and 4096, window 128.
+// Whether a request's SA path goes over its tokens in sigma's order: enough
+// window keys in all, four times its length, to be worth listing them.  Measured
+// (four requests, row kernel against order and what follows, us) at 2, 3, 4 and
+// 5 times: 65 to 78, 88 to 58, 105 to 77, 144 to 73 (32 q heads on 8 kv heads, d =
+// 128, length 16384, window 128), 44 to 170, 76 to 92, 84 to 98, 102 to 95 (window
+// 512), 28 to 43, 46 to 40, 45 to 34, 51 to 34 (4096, 128); 90 to 75, 114 to 73, 151
+// to 51, 176 to 56 (16 on 16, d = 64, 16384, 128).
 __host__ __device__ inline bool paged_sa_tiled(int n, int len, int half, int row_limit) {
-  return n > row_limit && (long long)n * (2LL * half + 1) >= 5LL * len;
+  return n > row_limit && (long long)n * (2LL * half + 1) >= 4LL * len;
 }
 inline bool paged_order_supported(const PagedProblem& pb) { return pb.B <= 1 << 27; }  // eight blocks each
+// Which of the two kernels over that order takes the request: a tile of Bt
+// members, perm_len / n places of sigma apart, against one member's window.
+// Measured (three requests, member against tile kernel, us, at Bt perm_len over
+// n (2 half + 1) of 32, 8, 7, 4 to 3.4, 2 and 0.5): 32 q heads on 8 kv heads,
+// d = 128: - , 57 to 84, 86 to 100, - , 119 to 91, 518 to 210; 16 on 16, d = 64:
+// 56 to 102, 71 to 106, - , - , 141 to 143, - ; 32 on 4, d = 64: - , - , - , 44 to
+// 59, - , 279 to 167 (at 0.3).
+__host__ __device__ inline bool paged_sa_members(int n, int Bt, int perm_len, int half) {
+  return (long long)Bt * perm_len >= 3LL * n * (2LL * half + 1);
+}
 size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit);
 // beside: the kernel before it in the stream is the SWA tile kernel of the same
 // call (or its join), beside which it may run.
 sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_tokens, void* workspace,
-                               SaOrder* order, bool beside, cudaStream_t stream);
+                               int group, SaOrder* order, bool beside, cudaStream_t stream);
 sa_status_t launch_paged_sa_tiles(const PagedProblem& pb, const SaOrder& order, const float* gate,
                                   const float* swa_part, void* workspace, int sms, cudaStream_t stream);
+
+// Member kernel (sa_paged_members.cu): the same by warp-level matrix
+// instructions, for members whose windows share little.
+bool paged_members_supported(const PagedProblem& pb);
+int paged_member_group(const PagedProblem& pb);      // members of a block
+size_t paged_member_groups(const PagedProblem& pb);  // entries of SaOrder::groups
+sa_status_t launch_paged_members(const PagedProblem& pb, const SaOrder& order, const float* gate,
+                                 const float* swa_part, cudaStream_t stream);
 
 // sigma^{-1} kernels.
 sa_status_t launch_inverse_perm(const int32_t* perm, int32_t* inv, int batch, int n,

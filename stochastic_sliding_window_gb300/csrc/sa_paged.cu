@@ -2,7 +2,7 @@
 // (block tables, slots and positions from the requests' lengths) and the
 // writer of new keys and values.  The attention itself is in
 // sa_paged_rows.cu and sa_paged_unit.cu (few new tokens) and sa_paged_tiles.cu
-// (many).
+// and sa_paged_members.cu (many).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -450,21 +450,31 @@ constexpr int kSwaRows = 16, kGatedRows = 64, kWideGatedRows = 32, kWideWindow =
 
 struct Choice {
   bool tiles;     // SWA (or the gated pair's SWA term) of requests beyond row_limit by tiles
-  bool sa_tiles;  // SA of such requests by tiles, where paged_sa_tiled says so
+  bool order;     // SA of such requests over sigma's order, where paged_sa_tiled says so:
+  bool sa_tiles;  //   some may go to the tile kernel,
+  bool members;   //   some to the member kernel (paged_sa_members)
   bool rows, unit;
   int row_limit;  // new tokens per request that the row kernel still takes
 };
 
 static Choice choose(const PagedProblem& pb, Path path, int kernel, int sms) {
-  Choice c{false, false, true, false, 0x7fffffff};
+  Choice c{false, false, false, false, true, false, 0x7fffffff};
   if (kernel != SA_PAGED_ROWS && paged_tiles_supported(pb)) {
-    if (kernel == SA_PAGED_TILES) return Choice{true, false, false, false, 0};
+    if (kernel == SA_PAGED_TILES) return Choice{true, false, false, false, false, false, 0};
     const int most = path == kPathSWA                                        ? kSwaRows
                      : path == kPathGated && pb.window_swa > kWideWindow ? kWideGatedRows
                                                                              : kGatedRows;
     const int limit = pb.g >= most ? 1 : most / pb.g;
-    if (pb.max_new > limit) c = Choice{path != kPathSA, path != kPathSWA, true, false, limit};
-    if (!paged_order_supported(pb)) c.sa_tiles = false;
+    if (pb.max_new > limit) {
+      c.tiles = path != kPathSA;
+      c.order = path != kPathSWA && paged_order_supported(pb);
+      c.row_limit = limit;
+    }
+    if (c.order) {  // (requests of limit + 1 to max_new new tokens)
+      const int bt = paged_tile_tokens(pb);
+      c.members = paged_members_supported(pb) && paged_sa_members(limit + 1, bt, pb.perm_len, pb.half);
+      c.sa_tiles = !c.members || !paged_sa_members(pb.max_new, bt, pb.perm_len, pb.half);
+    }
   }
   // few units of few keys: the unit kernel instead of the row kernel
   if (paged_unit_fits(pb, path, c.row_limit, sms)) {
@@ -488,6 +498,8 @@ static Workspace workspace_parts(const PagedProblem& pb, Path path, const Choice
   if (c.sa_tiles) {
     const size_t sa = round256(paged_tiles_workspace_bytes(pb, true, sms));
     w.tiles = w.tiles > sa ? w.tiles : sa;
+  }
+  if (c.order) {
     w.order = paged_order_workspace_bytes(pb, c.row_limit);
   }
   if (c.tiles && path == kPathGated) w.swa_part = round256(size_t(pb.T) * pb.Hq * pb.d * 4);
@@ -539,15 +551,16 @@ static sa_status_t run(const sa_paged_params_t* prm, Path path, const void* q, c
     st = launch_paged_tiles(pb, ch.row_limit, gate_swa, swa_part, w + parts.rows, sms, stream);
     if (st != SA_OK) return st;
   }
-  if (ch.sa_tiles) {
+  if (ch.order) {
     pb.sa_limit = ch.row_limit;
     SaOrder order;
-    st = launch_paged_order(pb, ch.row_limit, paged_tile_tokens(pb), w + parts.rows + parts.tiles, &order, ch.tiles,
-                            stream);
-    if (st == SA_OK) st = launch_paged_sa_tiles(pb, order, gate_sa, swa_part, w + parts.rows, sms, stream);
+    st = launch_paged_order(pb, ch.row_limit, paged_tile_tokens(pb), w + parts.rows + parts.tiles,
+                            ch.members ? paged_member_group(pb) : 0, &order, ch.tiles, stream);
+    if (st == SA_OK && ch.members) st = launch_paged_members(pb, order, gate_sa, swa_part, stream);
+    if (st == SA_OK && ch.sa_tiles) st = launch_paged_sa_tiles(pb, order, gate_sa, swa_part, w + parts.rows, sms, stream);
     if (st != SA_OK) return st;
   }
-  pb.beside = (ch.tiles || ch.sa_tiles) && path != kPathGated;  // (gated: it adds the SWA tiles' part)
+  pb.beside = (ch.tiles || ch.order) && path != kPathGated;  // (gated: it adds the SWA tiles' part)
   if (ch.unit) {
     st = launch_paged_unit(pb, path, ch.row_limit, swa_part, sms, stream);
     if (st != SA_OK) return st;

@@ -40,6 +40,7 @@ struct Params {
   int32_t* err;
   SaOrder order;
   uint2* words;  // [lists][cap / 32] of each 32 places: which are in the list, entries before them
+  int2* groups;  // SaOrder's
   int2* mark;    // [T] members in sigma's order, a request's from q_start on: place, position
   long long perm_stride, page_rows;
   int T, max_new, max_pages, page, num_pages, perm_len, half, row_limit, Bt, Hkv, lists, beside;
@@ -86,8 +87,17 @@ __device__ __forceinline__ void order_request(const Params& P) {
     if (tid == 0) atomicOr(P.err, SA_ERRBIT_RANGE);
     n = 0;
   }
+  const bool by_members = P.order.group > 0 && paged_sa_members(n, P.Bt, P.perm_len, P.half);
+  if (P.order.group > 0 && rank == 0) {
+    const int q0 = P.q_start[b], q1 = P.q_start[b + 1];
+    if (q0 >= 0 && q1 >= q0 && q1 <= P.T) {
+      const int base = q0 / P.order.group + b, end = q1 / P.order.group + b;
+      for (int s = base + tid; s <= end; s += kThreads)
+        P.groups[s] = by_members && (long long)(s - base) * P.order.group < n ? make_int2(b, s - base) : make_int2(-1, 0);
+    }
+  }
   if (n == 0) {  // (so for every block of the cluster)
-    if (tid == 0 && rank == 0) P.order.info[b] = make_int2(before, 0);
+    if (tid == 0 && rank == 0) P.order.info[b] = make_int4(before, 0, 0, 0);
     return;
   }
   const int q0 = P.q_start[b], c = len - n;
@@ -237,7 +247,7 @@ __device__ __forceinline__ void order_request(const Params& P) {
   }
   if (tid == 0) {
     chunks[tiles] = sum;
-    P.order.info[b] = make_int2(before, found);
+    P.order.info[b] = make_int4(before, by_members ? 0 : found, by_members ? found : 0, 0);
   }
 }
 
@@ -266,11 +276,12 @@ size_t word_bytes(const PagedProblem& pb, int row_limit) {
 size_t paged_order_workspace_bytes(const PagedProblem& pb, int row_limit) {
   const size_t n = size_t(lists(pb, row_limit)) * size_t(pb.perm_len);
   return round256(n * 8) + word_bytes(pb, row_limit) + round256(size_t(pb.T) * 24) +
-         round256((size_t(pb.T) + size_t(pb.B)) * 4) + round256(size_t(pb.B) * 8);
+         round256((size_t(pb.T) + size_t(pb.B)) * 4) + round256(size_t(pb.B) * 16) +
+         round256(paged_member_groups(pb) * 8);
 }
 
 sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_tokens, void* workspace,
-                               SaOrder* order, bool beside, cudaStream_t stream) {
+                               int group, SaOrder* order, bool beside, cudaStream_t stream) {
   const size_t n = size_t(lists(pb, row_limit)) * size_t(pb.perm_len);
   char* w = static_cast<char*>(workspace);
   order->list = reinterpret_cast<uint2*>(w);
@@ -284,7 +295,11 @@ sa_status_t launch_paged_order(const PagedProblem& pb, int row_limit, int tile_t
   w += round256(size_t(pb.T) * 24);
   order->chunks = reinterpret_cast<int32_t*>(w);
   w += round256((size_t(pb.T) + size_t(pb.B)) * 4);
-  order->info = reinterpret_cast<int2*>(w);
+  order->info = reinterpret_cast<int4*>(w);
+  w += round256(size_t(pb.B) * 16);
+  P.groups = reinterpret_cast<int2*>(w);
+  order->groups = P.groups;
+  order->group = group;
   order->cap = pb.perm_len;
   P.perm = pb.perm;
   P.table = pb.table;

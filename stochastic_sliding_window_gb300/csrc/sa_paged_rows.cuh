@@ -1,5 +1,5 @@
-// Device pieces shared by the two kernels for requests with few new tokens
-// (sa_paged_rows.cu, sa_paged_unit.cu): the request's fields, the warp-level
+// Device pieces shared by the kernels on the warp-level matrix instructions
+// (sa_paged_rows.cu, sa_paged_unit.cu, sa_paged_members.cu): the request's fields, the warp-level
 // matrix instructions, and one 16-key tile of the online softmax of a unit of
 // up to 16 query rows.
 #pragma once
@@ -205,12 +205,9 @@ struct Acc {
     }
   }
 
-  // 16 keys: K rows at sk, V rows behind them, their tokens in toks
-  // (0x7fffffff: no key); a row attends to tokens p - w + 1 .. p of its
-  // position p.  clear: every real row attends to all of them.
-  __device__ __forceinline__ void tile(uint32_t sk, const int* toks, unsigned w, bool clear, float scale_log2) {
+  // Scores, in log2 units, of 16 keys whose K rows are at sk.
+  __device__ __forceinline__ void scores(uint32_t sk, float scale_log2, float (&s)[NT][4]) const {
     const int lane = threadIdx.x & 31;
-    float s[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
     {
@@ -228,6 +225,15 @@ struct Acc {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] *= scale_log2;
     }
+  }
+
+  // 16 keys: K rows at sk, V rows behind them, their tokens in toks
+  // (0x7fffffff: no key); a row attends to tokens p - w + 1 .. p of its
+  // position p.  clear: every real row attends to all of them.
+  __device__ __forceinline__ void tile(uint32_t sk, const int* toks, unsigned w, bool clear, float scale_log2) {
+    const int lane = threadIdx.x & 31;
+    float s[NT][4];
+    scores(sk, scale_log2, s);
     if (!clear) {
       const int ta = toks[lane >> 2], tb = toks[(lane >> 2) + 8];
 #pragma unroll
@@ -238,6 +244,15 @@ struct Acc {
         if (unsigned(pos[t][1] - tb) >= w) s[t][3] = -INFINITY;
       }
     }
+    absorb<true>(sk, s);
+  }
+
+  // Takes 16 masked scores per row, and the V rows behind the K rows at sk, into
+  // the running softmax.  kLow: P's rounding to bf16 is made up for by a second
+  // product with what it left out.
+  template <bool kLow>
+  __device__ __forceinline__ void absorb(uint32_t sk, float (&s)[NT][4]) {
+    const int lane = threadIdx.x & 31;
     float x[NT][2];
     bool up = false;
 #pragma unroll
@@ -282,7 +297,7 @@ struct Acc {
         l[t][1] += p1;
         const uint32_t a = pack_bf16x2(p0, p1);
         hi[t][h] = transpose8(a);
-        lo[t][h] = transpose8(pack_bf16x2(p0 - __uint_as_float(a << 16), p1 - __uint_as_float(a & 0xffff0000u)));
+        if (kLow) lo[t][h] = transpose8(pack_bf16x2(p0 - __uint_as_float(a << 16), p1 - __uint_as_float(a & 0xffff0000u)));
       }
     }
     const uint32_t a = sk + (kKeys + (lane & 7) + (lane >> 4) * 8) * Pitch<D> + ((lane >> 3) & 1) * 16;
@@ -293,7 +308,7 @@ struct Acc {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma16816(o[i][t], vf, hi[t][0], hi[t][1]);
-        mma16816(o[i][t], vf, lo[t][0], lo[t][1]);
+        if (kLow) mma16816(o[i][t], vf, lo[t][0], lo[t][1]);
       }
     }
   }
