@@ -109,6 +109,43 @@ def test_sa_tiles(path, shape, window):
     assert torch.equal(out[:b.t], again[:b.t])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 2, 128), (3, 3, 64), (10, 2, 128), (32, 2, 64)])
+@pytest.mark.parametrize("path", ["sa", "gated"])
+def test_sa_of_requests_far_apart_and_close_in_one_call(path, hq, hkv, d):
+    """New tokens that are all of a long request, some of one and few of one:
+    their windows share much, little and nothing."""
+    b = Batch([1500, 300, 40, 1], [1600, 1400, 700, 90], hq, hkv, d, 32, seed=hq, perm_len=3001, behind=1)
+    out = torch.full((b.t + 1, hq, d), 2.0, dtype=torch.bfloat16, device="cuda")
+    err = err_word()
+    b.run(path, 128, 100, out=out, err=err, max_new=1500)
+    assert sa.check_error(err) == sa.SA_OK
+    b.check(out, path, 128, 100, weight_bits=8, what=path)
+    assert (out[b.t:] == 2.0).all()
+    assert torch.equal(b.run(path, 128, 100)[:b.t], out[:b.t])
+
+
+def test_members_with_bad_sigma_and_pages():
+    """As for tiles: bad pages' keys are left out and reported, rows that a bad
+    sigma does not name are left as they were."""
+    b = Batch([200], [1500], 4, 2, 128, 16, seed=2, perm_len=6000)
+    good = b.run("sa", 300).clone()
+    table = b.args[3].clone()
+    table[0, 3:9] = -5
+    table[0, 60:] = 1 << 30
+    args = list(b.args)
+    args[3] = table
+    err = err_word()
+    out = sa.sa_paged_forward(*args, b.perm_d, b.inv_d, window=300, err=err)
+    assert sa.check_error(err) == sa.SA_ERR_BAD_PERM and torch.isfinite(out).all()
+    perm = b.perm_d.clone()
+    perm[0, perm[0] == 1400] = 7  # token 1400 named nowhere
+    err.zero_()
+    out = torch.full_like(good, 3.0)
+    sa.sa_paged_forward(*b.args, perm, b.inv_d, window=300, out=out, err=err)
+    assert sa.check_error(err) == sa.SA_ERR_BAD_PERM
+    assert (out == 3.0).all(-1).all(-1).sum() == 1
+
+
 def test_sa_tiles_with_bad_sigma_and_pages():
     b = Batch([200], [500], 4, 2, 64, 16, seed=2, perm_len=600)
     good = b.run("sa", 64).clone()
