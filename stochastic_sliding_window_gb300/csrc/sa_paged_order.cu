@@ -1,5 +1,5 @@
-// A request's tokens in sigma's order, for the SA tiles of the paged-cache
-// attention (sa_paged_tiles.cu).
+// A request's tokens in sigma's order, for SA of many new tokens over a paged
+// cache (sa_paged_members.cu, sa_paged_tiles.cu).
 //
 // For each request that brings many new tokens, a cluster of eight blocks
 // passes over its row of sigma, an eighth each, and keeps, in order, the entries

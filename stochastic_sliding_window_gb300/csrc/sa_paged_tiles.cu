@@ -38,6 +38,7 @@
 // other, its keys the list from the first one's window to the last one's, and
 // the rest is as for SWA, but for the causal rule among the new tokens
 // themselves (older keys precede every row) and rows that TMA cannot box.
+// (Members far apart share little: sa_paged_members.cu takes those requests.)
 //
 // Split.  One block per SM.  All chunks of all tiles, laid end to end
 // (request, kv head, tile, chunk), are cut into equal runs, one per block, so
