@@ -19,8 +19,8 @@
 // tile kernel; sums and O are fp32.
 //
 // Measured: three chunks of up to 501 tokens at 12000, 16 heads of d = 64, window
-// 256, 48 to 52 us a call (79 by the tile kernel); two of up to 1024 at 16384, 32 q
-// heads on 8 kv heads, d = 128, window 128, 55 us (70).  Blocks of 64 rows that
+// 256, 45 to 49 us a call (79 by the tile kernel); two of up to 1024 at 16384, 32 q
+// heads on 8 kv heads, d = 128, window 128, 49 us (70).  Blocks of 64 rows that
 // share their stages read a third less, but their warps wait for each other at
 // every stage: 96 us for the first.
 #include "sa_paged_rows.cuh"
@@ -30,7 +30,9 @@
 namespace sa {
 namespace prow {
 
-constexpr int kMemberWarps = 2;  // (blocks of four: 91 instead of 89.5 us for a gated chunk)
+// A block is one warp, so that a finished one makes room at once: a gated chunk
+// 85 us, with blocks of two and four warps 91 and 92.
+constexpr int kMemberWarps = 1;
 constexpr int kMemberThreads = 32 * kMemberWarps;
 constexpr int kMemberRows = 16;
 // Three stages where that leaves 16 warps an SM: 52 instead of 57 us for SA chunks
@@ -54,7 +56,7 @@ struct MemberParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMemberThreads, D == 64 ? 8 : 6)
+__global__ void __launch_bounds__(kMemberThreads, D == 64 ? 16 : 12)
     sa_paged_members_kernel(const __grid_constant__ MemberParams P) {
   constexpr int kPitch = Pitch<D>;
   constexpr int kCpr = D / 8;
